@@ -176,6 +176,94 @@ int moe_glu_forward(const void* X, const float* gate_logits, int top_k, const vo
                     int64_t P, int E, int act, tffn_routing* routing, struct CUstream_st* stream);
 
 /*
+ * Training operators.  The pages describe the forward block; these complete a
+ * training step of its pre-norm form, Y = X + FFN(LN(X)): the norm on both
+ * sides of the residual add, the gated FFN with what its backward pass needs,
+ * that backward pass, and the orthogonalisation that the Muon optimiser
+ * applies to a weight's update.  Results repeat bit for bit (no atomics on
+ * values).  Tensors of one call must not overlap except where said.
+ */
+
+/* Element types of activations and parameters. */
+typedef enum { TFFN_BF16 = 0, TFFN_F32 = 1 } tffn_dtype;
+
+/*
+ * layer_norm_forward -- S = X + R; Y = (S - mean) rstd gamma + beta per row,
+ * mean the row's mean, rstd = 1 / sqrt(mean((S - mean)^2) + eps).
+ *
+ *   X, R [T x N] dtype (R nullable: S is X and is not written)
+ *   gamma, beta [N] param_dtype (nullable: 1 and 0)
+ *   Y, S [T x N] dtype      mean, rstd [T] fp32
+ *   eps >= 0; N >= 1, T >= 0; pointers aligned to their element type only
+ *   (rows that start on 16-byte boundaries are faster).
+ * Numerics: sums in fp32; S is rounded to its type before the norm is taken,
+ * so the backward pass sees the same S.  S may alias X or R, and Y may alias
+ * X when R is NULL.
+ */
+int layer_norm_forward(const void* X, const void* R, const void* gamma, const void* beta, float eps, int dtype,
+                       int param_dtype, int64_t T, int64_t N, void* Y, void* S, float* mean, float* rstd,
+                       struct CUstream_st* stream);
+
+/*
+ * layer_norm_backward -- with xh = (S - mean) rstd and g = dY gamma:
+ *   dX = rstd (g - mean(g) - xh mean(g xh)) + dS   [T x N] dtype
+ *   dgamma = sum over rows of dY xh, dbeta = sum over rows of dY   [N] fp32
+ * dS [T x N] (nullable) is the gradient that reaches S past the norm, through
+ * the residual; dX is then the gradient of X and of R.  dgamma and dbeta are
+ * both given or both NULL.  Sums in fp32.  Workspace:
+ * layer_norm_workspace_bytes(T, N).
+ */
+int layer_norm_backward(const void* dY, const void* S, const void* gamma, const float* mean, const float* rstd,
+                        const void* dS, int dtype, int param_dtype, int64_t T, int64_t N, void* dX, float* dgamma,
+                        float* dbeta, struct CUstream_st* stream);
+size_t layer_norm_workspace_bytes(int64_t T, int64_t N);
+
+/*
+ * ffn_glu_forward_train -- ffn_glu_forward that keeps what the backward pass
+ * needs: G = X W1 and U = X W3 [M x O] bf16, Y = (act(G) * U) W2.  Shapes,
+ * alignment and errors as ffn_glu_forward.
+ * Numerics: H = act(G) * U is formed from the fp32 sums and rounded to bf16
+ * once; G and U are rounded when they are stored.  Workspace:
+ * ffn_glu_train_workspace_bytes(M, O).
+ */
+int ffn_glu_forward_train(const void* X, const void* W1, const void* W3, const void* W2, int act, int64_t M,
+                          int64_t N, int64_t O, int64_t P, void* Y, void* G, void* U, struct CUstream_st* stream);
+
+/*
+ * ffn_glu_backward -- gradients of the gated FFN from dY [M x P], the forward
+ * pass's operands and its G and U:
+ *   dH = dY W2^T; dU = dH * act(G); dG = dH * U * act'(G)
+ *   dX = dG W1^T + dU W3^T [M x N]       dW2 = (act(G) * U)^T dY [O x P]
+ *   dW1 = X^T dG, dW3 = X^T dU [N x O]   all bf16, rounded once
+ * ReLU's derivative at 0 is 0.  M = 0 sets the weights' gradients to zero.
+ * Numerics: products accumulate in fp32; dG, dU and H are rounded to bf16
+ * where they become operands of the next products.  Workspace:
+ * ffn_glu_train_workspace_bytes(M, O).
+ */
+int ffn_glu_backward(const void* dY, const void* X, const void* W1, const void* W3, const void* W2, const void* G,
+                     const void* U, int act, int64_t M, int64_t N, int64_t O, int64_t P, void* dX, void* dW1,
+                     void* dW3, void* dW2, struct CUstream_st* stream);
+size_t ffn_glu_train_workspace_bytes(int64_t M, int64_t O);
+
+/*
+ * muon_orthogonalize -- Newton-Schulz iteration of the Muon optimiser (K.
+ * Jordan, 2024) on each of `batch` matrices G [m x n] (dtype, dense):
+ *   X = G / (|G|_F + 1e-7); steps times: A = X X^T, X = a X + (b A + c A A) X
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315); a tall matrix (m > n) goes
+ * through its transpose.  out [batch x m x n] bf16: singular values of G that
+ * are not negligible end near 1.
+ *   1 <= steps <= 64; m, n <= 262144; batch <= 65535; G aligned to its type,
+ *   out to 2 bytes (n a multiple of 8 and out on 16 bytes save a copy).
+ * Numerics: products accumulate in fp32; X, A and b A + c A A are fp16
+ * between them (eight times bf16's resolution), X scaled by 64.  Directions
+ * more than ~1e4 below the largest are dominated by that rounding.
+ * Workspace: muon_workspace_bytes(batch, m, n).
+ */
+int muon_orthogonalize(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int steps, void* out,
+                       struct CUstream_st* stream);
+size_t muon_workspace_bytes(int64_t batch, int64_t m, int64_t n);
+
+/*
  * ffn_forward_decode_noalloc -- ffn_forward for M <= 32 rows (the decode
  * shapes) that allocates nothing.  The paper has no counterpart: this entry
  * point exists for callers that cannot allocate device memory -- plugins

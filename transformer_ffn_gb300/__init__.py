@@ -14,7 +14,10 @@ import torch
 __all__ = ["ffn_forward", "moe_ffn_forward", "load", "check", "set_option", "workspace_bytes",
            "set_workspace", "last_launch_count", "timing_begin", "timing_end", "TffnError",
            "ACT_NONE", "ACT_RELU", "ACT_GELU_TANH", "ACT_SILU", "ffn_glu_forward", "moe_glu_forward", "OPT_PATH", "OPT_WAIT_LIMIT_MS",
-           "OPT_SKIP_FLAG", "OPT_GROUP_M", "OPT_MOE_ORDER", "OPT_MOE_COMBINE", "LIB_PATH"]
+           "OPT_SKIP_FLAG", "OPT_GROUP_M", "OPT_MOE_ORDER", "OPT_MOE_COMBINE", "LIB_PATH",
+           "layer_norm_forward", "layer_norm_backward", "ffn_glu_forward_train", "ffn_glu_backward",
+           "muon_orthogonalize", "layer_norm_workspace_bytes", "ffn_glu_train_workspace_bytes",
+           "muon_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtffn.so")
@@ -84,6 +87,23 @@ def load():
     L.tffn_debug_tiles.restype = None
     L.tffn_debug_stream_plan.argtypes = [i32, i64, i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int64)]
     L.tffn_debug_stream_plan.restype = i32
+    f32 = ctypes.c_float
+    L.layer_norm_forward.argtypes = [vp, vp, vp, vp, f32, i32, i32, i64, i64, vp, vp, vp, vp, vp]
+    L.layer_norm_forward.restype = i32
+    L.layer_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp]
+    L.layer_norm_backward.restype = i32
+    L.layer_norm_workspace_bytes.argtypes = [i64, i64]
+    L.layer_norm_workspace_bytes.restype = ctypes.c_size_t
+    L.ffn_glu_forward_train.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp]
+    L.ffn_glu_forward_train.restype = i32
+    L.ffn_glu_backward.argtypes = [vp] * 7 + [i32, i64, i64, i64, i64] + [vp] * 5
+    L.ffn_glu_backward.restype = i32
+    L.ffn_glu_train_workspace_bytes.argtypes = [i64, i64]
+    L.ffn_glu_train_workspace_bytes.restype = ctypes.c_size_t
+    L.muon_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp]
+    L.muon_orthogonalize.restype = i32
+    L.muon_workspace_bytes.argtypes = [i64, i64, i64]
+    L.muon_workspace_bytes.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -259,6 +279,187 @@ def moe_glu_forward(X, gate_logits, top_k, W1, W3, W2, act="silu", out=None, rou
                            E, _act(act), rp, _stream_ptr(stream))
     _raise(rc, "moe_glu_forward")
     return (Y, r) if routing else Y
+
+
+# ------------------------------------------------------------ training operators
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _check_tensor(name, t, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _check_lead(name, t, dims, dtypes):
+    """The tensor that fixes a call's device and types."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} must have {' or '.join(str(d) for d in dims)} dimensions")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
+
+
+class _OnStream:
+    """A call's stream: results are allocated on it, and torch is told that it
+    uses the operands, so that their memory is not handed out too early."""
+
+    def __init__(self, stream, *operands):
+        self.stream = stream
+        if stream is not None and stream != torch.cuda.current_stream():
+            for t in operands:
+                if t is not None:
+                    t.record_stream(stream)
+        else:
+            self.stream = None
+        self.ptr = _stream_ptr(stream)
+
+    def empty(self, shape, dtype, device):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_norm_param(name, t, N, dev):
+    _check_tensor(name, t, t.dtype if getattr(t, "dtype", None) in _DTYPES else torch.float32, (N,), dev)
+
+
+def layer_norm_forward(X, gamma, beta, residual=None, eps=1e-5, stream=None):
+    """(Y, S, mean, rstd): S = X + residual (X itself without one), Y = (S - mean)
+    * rstd * gamma + beta over the rows of S [T, N].  X, residual, Y and S are
+    bfloat16 or float32; gamma and beta [N] are bfloat16 or float32, or None;
+    mean and rstd [T] are float32."""
+    L = load()
+    _check_lead("X", X, (2,), (torch.bfloat16, torch.float32))
+    dev = X.device
+    T, N = X.shape
+    par = gamma if gamma is not None else beta
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _check_norm_param(name, t, N, dev)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have the same type")
+    if residual is not None:
+        _check_tensor("residual", residual, X.dtype, X.shape, dev)
+    on = _OnStream(stream, X, residual, gamma, beta)
+    Y = on.empty((T, N), X.dtype, dev)
+    S = X if residual is None else on.empty((T, N), X.dtype, dev)
+    stats = on.empty((2, T), torch.float32, dev)
+    mean, rstd = stats[0], stats[1]
+    rc = L.layer_norm_forward(_ptr(X), _ptr(residual), _ptr(gamma), _ptr(beta), float(eps), _DTYPES[X.dtype],
+                              _DTYPES[par.dtype] if par is not None else 0, T, N, _ptr(Y),
+                              _ptr(S) if residual is not None else None, _ptr(mean), _ptr(rstd), on.ptr)
+    _raise(rc, "layer_norm_forward")
+    return Y, S, mean, rstd
+
+
+def layer_norm_backward(dY, S, gamma, mean, rstd, dS=None, weight_grads=True, stream=None):
+    """(dX, dgamma, dbeta) of layer_norm_forward: dX is the gradient of X (and of
+    the residual), with dS, the gradient that reaches S past the norm, added;
+    dgamma and dbeta are float32 (None without weight_grads)."""
+    L = load()
+    _check_lead("dY", dY, (2,), (torch.bfloat16, torch.float32))
+    dev = dY.device
+    T, N = dY.shape
+    _check_tensor("S", S, dY.dtype, dY.shape, dev)
+    if gamma is not None:
+        _check_norm_param("gamma", gamma, N, dev)
+    _check_tensor("mean", mean, torch.float32, (T,), dev)
+    _check_tensor("rstd", rstd, torch.float32, (T,), dev)
+    if dS is not None:
+        _check_tensor("dS", dS, dY.dtype, dY.shape, dev)
+    on = _OnStream(stream, dY, S, gamma, mean, rstd, dS)
+    dX = on.empty((T, N), dY.dtype, dev)
+    dgamma = dbeta = None
+    if weight_grads:
+        dgamma, dbeta = on.empty((N,), torch.float32, dev), on.empty((N,), torch.float32, dev)
+    rc = L.layer_norm_backward(_ptr(dY), _ptr(S), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dS), _DTYPES[dY.dtype],
+                               _DTYPES[gamma.dtype] if gamma is not None else 0, T, N, _ptr(dX), _ptr(dgamma),
+                               _ptr(dbeta), on.ptr)
+    _raise(rc, "layer_norm_backward")
+    return dX, dgamma, dbeta
+
+
+def _check_glu_weights(X, W1, W3, W2):
+    dev, bf = X.device, torch.bfloat16
+    N = X.shape[1]
+    if not isinstance(W1, torch.Tensor) or W1.dim() != 2 or not isinstance(W2, torch.Tensor) or W2.dim() != 2:
+        raise ValueError("W1 and W2 must be 2-dimensional tensors")
+    O, P = W1.shape[1], W2.shape[1]
+    for name, t, shape in (("W1", W1, (N, O)), ("W3", W3, (N, O)), ("W2", W2, (O, P))):
+        _check_tensor(name, t, bf, shape, dev)
+    return N, O, P
+
+
+def ffn_glu_forward_train(X, W1, W3, W2, act="silu", stream=None):
+    """(Y, G, U): the gated FFN Y = (act(G) * U) @ W2 with G = X @ W1 and U = X @ W3
+    kept for ffn_glu_backward; all bfloat16."""
+    L = load()
+    _check_lead("X", X, (2,), (torch.bfloat16,))
+    N, O, P = _check_glu_weights(X, W1, W3, W2)
+    M = X.shape[0]
+    on = _OnStream(stream, X, W1, W3, W2)
+    Y, G, U = (on.empty((M, c), torch.bfloat16, X.device) for c in (P, O, O))
+    rc = L.ffn_glu_forward_train(_ptr(X), _ptr(W1), _ptr(W3), _ptr(W2), _act(act), M, N, O, P, _ptr(Y), _ptr(G),
+                                 _ptr(U), on.ptr)
+    _raise(rc, "ffn_glu_forward_train")
+    return Y, G, U
+
+
+def ffn_glu_backward(dY, X, W1, W3, W2, G, U, act="silu", stream=None):
+    """(dX, dW1, dW3, dW2), all bfloat16: the gradients of ffn_glu_forward_train from
+    Y's gradient, the forward pass's operands and its G and U."""
+    L = load()
+    _check_lead("X", X, (2,), (torch.bfloat16,))
+    N, O, P = _check_glu_weights(X, W1, W3, W2)
+    M, dev, bf = X.shape[0], X.device, torch.bfloat16
+    for name, t, cols in (("dY", dY, P), ("G", G, O), ("U", U, O)):
+        _check_tensor(name, t, bf, (M, cols), dev)
+    on = _OnStream(stream, dY, X, W1, W3, W2, G, U)
+    dX, dW1, dW3, dW2 = (on.empty(shape, bf, dev) for shape in ((M, N), (N, O), (N, O), (O, P)))
+    rc = L.ffn_glu_backward(_ptr(dY), _ptr(X), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(G), _ptr(U), _act(act), M, N, O, P,
+                            _ptr(dX), _ptr(dW1), _ptr(dW3), _ptr(dW2), on.ptr)
+    _raise(rc, "ffn_glu_backward")
+    return dX, dW1, dW3, dW2
+
+
+def muon_orthogonalize(G, steps=5, stream=None):
+    """The Muon optimiser's Newton-Schulz orthogonalisation of a matrix [m, n] or a
+    stack of matrices [batch, m, n] (bfloat16 or float32), in bfloat16."""
+    L = load()
+    _check_lead("G", G, (2, 3), (torch.bfloat16, torch.float32))
+    m, n = G.shape[-2:]
+    on = _OnStream(stream, G)
+    out = on.empty(G.shape, torch.bfloat16, G.device)
+    rc = L.muon_orthogonalize(_ptr(G), _DTYPES[G.dtype], G.shape[0] if G.dim() == 3 else 1, m, n, int(steps),
+                              _ptr(out), on.ptr)
+    _raise(rc, "muon_orthogonalize")
+    return out
+
+
+def layer_norm_workspace_bytes(T, N):
+    return int(load().layer_norm_workspace_bytes(T, N))
+
+
+def ffn_glu_train_workspace_bytes(M, O):
+    return int(load().ffn_glu_train_workspace_bytes(M, O))
+
+
+def muon_workspace_bytes(batch, m, n):
+    return int(load().muon_workspace_bytes(batch, m, n))
 
 
 def check(stream=None):

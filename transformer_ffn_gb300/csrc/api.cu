@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/tffn.h"
+#include "api.h"
 #include "decode.cuh"
 #include "wstream.cuh"
 #include "engine.cuh"
@@ -474,6 +475,51 @@ void fill_layer(engine::LayerArgs& la, int64_t K, int64_t ncols, int act, int ou
 namespace tffn {
 uint64_t option_wait_limit_ns() { return wait_limit_ns(); }
 int32_t option_skip_flag() { return static_cast<int32_t>(g_opt_skip.load()); }
+
+std::mutex& api_mutex() { return g_mu; }
+
+int api_space(size_t data_bytes, cudaStream_t s, ApiSpace* out)
+{
+    DeviceState* d = nullptr;
+    int rc = device_state(&d);
+    if (rc != TFFN_OK)
+        return rc;
+    uint8_t* base = nullptr;
+    rc = workspace(*d, SYNC_BYTES + data_bytes, s, &base);
+    if (rc != TFFN_OK)
+        return rc;
+    out->ctrl = reinterpret_cast<DevCtrl*>(base);
+    out->counters = reinterpret_cast<uint32_t*>(base + OFF_DCOUNT);
+    out->counter_words = DCOUNT_WORDS;
+    out->data = base + SYNC_BYTES;
+    return TFFN_OK;
+}
+
+int api_sms(int* sms)
+{
+    DeviceState* d = nullptr;
+    const int rc = device_state(&d);
+    if (rc == TFFN_OK)
+        *sms = d->sms;
+    return rc;
+}
+
+size_t api_sync_bytes() { return SYNC_BYTES; }
+
+int api_encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle)
+{
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return g_encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? 0
+               : -1;
+}
+
+void api_launches(int n) { g_last_launches = n; }
+void api_timing_start(cudaStream_t s) { timing_start(s); }
+void api_timing_stop(cudaStream_t s) { timing_stop(s); }
 }  // namespace tffn
 
 // Key of a dense-FFN call: everything its kernel parameters depend on.

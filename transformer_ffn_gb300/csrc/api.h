@@ -1,0 +1,48 @@
+// api.h -- what the entry points outside api.cu share with it: the library's
+// lock, the current device's workspace, tensor-map encoding, the launch count
+// and the timing events.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+#include <mutex>
+
+namespace tffn {
+
+struct DevCtrl;
+
+// The current device's workspace.  Counters are zero between calls: a kernel
+// that uses them leaves them at zero.
+struct ApiSpace {
+    DevCtrl* ctrl;
+    uint32_t* counters;
+    size_t counter_words;
+    uint8_t* data;
+};
+
+// Held by every entry point from its first use of the workspace to its last launch.
+std::mutex& api_mutex();
+
+// The workspace with at least `data_bytes` behind its sync region (a
+// tffn_status; under the lock).
+int api_space(size_t data_bytes, cudaStream_t s, ApiSpace* out);
+
+// SMs of the current device.
+int api_sms(int* sms);
+
+// Bytes of the workspace in front of its data.
+size_t api_sync_bytes();
+
+// cuTensorMapEncodeTiled with unit element strides, 256-byte L2 promotion and
+// zero fill; 0 or -1.
+int api_encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
+
+void api_launches(int n);
+void api_timing_start(cudaStream_t s);
+void api_timing_stop(cudaStream_t s);
+
+}  // namespace tffn

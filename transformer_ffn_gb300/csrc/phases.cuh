@@ -1,0 +1,831 @@
+// phases.cuh -- a persistent 2-SM tcgen05 kernel that runs a table of dependent
+// matrix products in one launch: the gated FFN's training forward and backward
+// passes and the Newton-Schulz steps of muon_orthogonalize.
+//
+// A phase is D = A B over 256 x 256 output tiles with fp32 accumulation in
+// tensor memory.  Either operand may be stored with its reduction index
+// contiguous (K-major) or with its row / column index contiguous (MN-major), so
+// the products with transposed operands of a backward pass read the caller's
+// row-major tensors where they lie; nothing is transposed in memory.  A phase
+// may add a second K segment (dX = dG W1^T + dU W3^T is one accumulation), may
+// split K over several tasks whose fp32 partial tiles the last one adds in
+// part order, and may compute only the lower triangle of a symmetric result
+// and store each tile twice.
+//
+// Order and dependencies: tickets run through the phases in table order.  A
+// phase that reads what an earlier phase wrote waits on that phase's tile
+// counts: per 256-row band of its output, or all of it.  Every wait points to
+// smaller tickets, so the launch finishes with any number of resident CTAs.
+//
+// Roles, tiles, rings and tensor-memory accumulators are those of the FFN
+// engine (engine.cuh): clusters of two CTAs, six 32 KiB stages per CTA, an A
+// loader that claims tickets one task ahead, a B loader, one MMA thread, four
+// epilogue warps with two 4 KiB staging buffers each.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "engine.cuh"
+#include "phases_params.cuh"
+
+namespace tffn {
+namespace phases {
+
+using engine::A_STAGE_BYTES;
+using engine::arrive_on_leader;
+using engine::AUX_BYTES;
+using engine::B_BOX_BYTES;
+using engine::B_LOADER_WARP;
+using engine::BM_CTA;
+using engine::NUM_THREADS;
+using engine::OUT_BUF_BYTES;
+using engine::OUT_BYTES;
+using engine::out_buffer_free;
+using engine::out_store_box;
+using engine::Ring;
+using engine::STAGE_BYTES;
+using engine::stage_half;
+using engine::STAGES;
+using engine::TASK_CONSUMERS;
+using engine::TASK_SLOTS;
+using engine::TMEM_COLS;
+using engine::wait_own;
+
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + AUX_BYTES + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+
+struct Aux {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t task_full[TASK_SLOTS];
+    uint64_t task_empty[TASK_SLOTS];
+    uint64_t drain;
+    int4 task[TASK_SLOTS];
+    uint32_t tmem_base;
+    uint32_t abort;
+};
+static_assert(sizeof(Aux) <= AUX_BYTES, "aux block fits");
+
+// A task: x = phase (-1: no more work), y = row tile, z = column tile,
+// w = batch * 256 + K part.
+__device__ __forceinline__ int task_batch(const int4& t) { return t.w >> 8; }
+__device__ __forceinline__ int task_part(const int4& t) { return t.w & 255; }
+
+__device__ __forceinline__ int4 decode_ticket(const Params& p, int32_t t)
+{
+    if (t >= p.total)
+        return make_int4(-1, 0, 0, 0);
+    int ip = 0;
+    while (ip + 1 < p.n_phases && t >= p.ph[ip + 1].first)
+        ++ip;
+    const Phase& f = p.ph[ip];
+    int32_t i = t - f.first;
+    int32_t part = 0;
+    if (f.splits > 1) {
+        part = i % f.splits;
+        i /= f.splits;
+    }
+    const int32_t tiles = f.sym ? f.m_tiles * (f.m_tiles + 1) / 2 : f.m_tiles * f.n_tiles;
+    int32_t batch = 0;
+    if (f.batches > 1) {
+        batch = i / tiles;
+        i -= batch * tiles;
+    }
+    int32_t m, n;
+    if (f.sym) {
+        // row m of the triangle starts at m (m + 1) / 2
+        m = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
+        while (m * (m + 1) / 2 > i)
+            --m;
+        while ((m + 1) * (m + 2) / 2 <= i)
+            ++m;
+        n = i - m * (m + 1) / 2;
+    } else {
+        const int32_t per = f.group_m * f.n_tiles;
+        const int32_t g = i / per;
+        i -= g * per;
+        const int32_t g0 = g * f.group_m;
+        const int32_t size = f.m_tiles - g0 < f.group_m ? f.m_tiles - g0 : f.group_m;
+        n = i / size;
+        m = g0 + i - n * size;
+    }
+    return make_int4(ip, f.m_first + m, n, batch * 256 + part);
+}
+
+// k-blocks [k0, k1) of a K part.
+__device__ __forceinline__ void part_range(const Phase& f, int part, int& k0, int& k1)
+{
+    const int nk = f.nk[0] + f.nk[1];
+    k0 = 0;
+    k1 = nk;
+    if (f.splits > 1) {
+        k0 = nk * part / f.splits;
+        k1 = nk * (part + 1) / f.splits;
+    }
+}
+
+// Poll (acquire, gpu scope) until the counter reaches its target, then order
+// this thread's TMA loads after it.  `known` remembers the last counter seen
+// complete.
+static __device__ __noinline__ bool wait_count_timed(const WaitCtx& w, const uint32_t* ctr, uint32_t target,
+                                                     uint32_t info)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::ld_acquire_gpu(ctr) < target) {
+        if (*w.abort)
+            return false;
+        if (ptx::globaltimer() - t0 > w.limit_ns) {
+            raise_error(w, static_cast<uint32_t>(TFFN_ERR_TIMEOUT), SITE_H_FLAG, info);
+            return false;
+        }
+        __nanosleep(32);
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool wait_dep(const Params& p, const WaitCtx& w, const Dep& d, int batch, int band,
+                                         int32_t& known)
+{
+    if (d.mode == DEP_NONE)
+        return true;
+    const int32_t idx = d.base + batch * d.stride + (d.mode == DEP_BAND ? 1 + band : 0);
+    if (idx == known)
+        return true;
+    const uint32_t target = static_cast<uint32_t>(d.mode == DEP_BAND ? d.target_band : d.target_all);
+    if (!wait_count_timed(w, p.counters + idx, target, static_cast<uint32_t>(idx)))
+        return false;
+    ptx::fence_proxy_async_global();
+    known = idx;
+    return true;
+}
+
+// One operand's 128 rows (columns) x 64 k of a stage.
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t fb, int32_t k, int32_t mn,
+                                             int32_t z, bool mn_major, bool four)
+{
+    if (!mn_major) {
+        ptx::tma_load_3d_pair(dst, map, fb, k, mn, z);
+    } else if (four) {
+        ptx::tma_load_4d_pair(dst, map, fb, 0, k, mn / 64, z);
+    } else {
+        ptx::tma_load_3d_pair(dst, map, fb, mn, k, z);
+        ptx::tma_load_3d_pair(dst + B_BOX_BYTES, map, fb, mn + 64, k, z);
+    }
+}
+
+// ----------------------------------------------------------------- loaders
+// A loader of one CTA; the leader's also claims the tickets (one task ahead,
+// so the hand-over of the next task never waits for the claim).
+__device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+{
+    uint32_t stage = 0, phase = 0;
+    int32_t known = -1;
+    Ring ring;
+    int32_t last_phase[STAGES];
+    for (int s = 0; s < STAGES; ++s)
+        last_phase[s] = -1;
+    auto claim_publish = [&](int4& out) -> bool {
+        out = decode_ticket(p, static_cast<int32_t>(atomicAdd(&p.ctrl->ticket, 1u)));
+        if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_empty[ring.slot]), ring.phase ^ 1u, SITE_TASK_EMPTY))
+            return false;
+        engine::publish_task(aux, ring, out);
+        return true;
+    };
+    int4 ahead = make_int4(-1, 0, 0, 0);
+    const bool started = rank != 0 || claim_publish(ahead);
+    while (started) {
+        int4 task;
+        if (rank == 0) {
+            task = ahead;
+            if (task.x >= 0 && !claim_publish(ahead))
+                break;
+        } else if (!engine::read_task(aux, w, ring, rank, false, 0, task)) {
+            break;
+        }
+        if (task.x < 0)
+            break;
+        const Phase& f = p.ph[task.x];
+        const int32_t batch = task_batch(task);
+        const int32_t row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA;
+        const bool mn = f.a_mn != 0, four = f.a4 != 0;
+        const int nk0 = f.nk[0];
+        const CUtensorMap* map0 = &p.map[f.map_a[0]];
+        const CUtensorMap* map1 = &p.map[f.map_a[1]];
+        int k0, k1;
+        part_range(f, task_part(task), k0, k1);
+        if (!wait_dep(p, w, f.dep_a, batch, task.y, known))
+            break;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            ok = wait_mbar(w, ptx::smem_u32(&aux.empty[stage]), phase ^ 1u, SITE_SMEM_EMPTY);
+            if (!ok)
+                break;
+            const uint32_t fb_local = ptx::smem_u32(&aux.full[stage]);
+            const uint32_t fb = ptx::mapa(fb_local, 0);   // the leader's stage barrier
+            if (rank == 0)
+                ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
+            const bool second = kb >= nk0;
+            load_operand(ptx::smem_u32(stages + stage * STAGE_BYTES), second ? map1 : map0, fb,
+                         (second ? kb - nk0 : kb) * BK, row0, batch, mn, four);
+            last_phase[stage] = static_cast<int32_t>(phase);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok)
+            break;
+    }
+    // Exit: every copy of the pair has landed (the leader's stage barriers
+    // count both CTAs' bytes; the peer cannot leave before the final cluster
+    // barrier).
+    if (rank == 0)
+        for (int s = 0; s < STAGES; ++s)
+            if (last_phase[s] >= 0)
+                wait_own(w, ptx::smem_u32(&aux.full[s]), static_cast<uint32_t>(last_phase[s]));
+}
+
+__device__ void run_b_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+{
+    uint32_t stage = 0, phase = 0;
+    int32_t known = -1;
+    Ring ring;
+    for (;;) {
+        int4 task;
+        if (!engine::read_task(aux, w, ring, rank, false, 0, task) || task.x < 0)
+            break;
+        const Phase& f = p.ph[task.x];
+        const int32_t batch = task_batch(task);
+        // A gated tile pairs 128 columns of W1 (the leader's half) with the
+        // same 128 columns of W3 (the peer's half).
+        const bool gated = f.epi == EPI_GLU_SAVE;
+        const int32_t col0 = gated ? task.z * BN_CTA : task.z * BN + static_cast<int32_t>(rank) * BN_CTA;
+        const CUtensorMap* map0 = &p.map[f.map_b[gated ? rank : 0]];
+        const CUtensorMap* map1 = &p.map[f.map_b[1]];
+        const bool mn = f.b_mn != 0, four = f.b4 != 0;
+        const int nk0 = f.nk[0];
+        int k0, k1;
+        part_range(f, task_part(task), k0, k1);
+        if (!wait_dep(p, w, f.dep_b, batch, task.z, known))
+            return;
+        for (int kb = k0; kb < k1; ++kb) {
+            if (!wait_mbar(w, ptx::smem_u32(&aux.empty[stage]), phase ^ 1u, SITE_SMEM_EMPTY))
+                return;
+            const uint32_t fb = ptx::mapa(ptx::smem_u32(&aux.full[stage]), 0);
+            const bool second = kb >= nk0;
+            load_operand(ptx::smem_u32(stages + stage * STAGE_BYTES) + A_STAGE_BYTES, second ? map1 : map0, fb,
+                         (second ? kb - nk0 : kb) * BK, col0, batch, mn, four);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- leader: MMA
+__device__ void run_mma(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t tmem_base)
+{
+    uint32_t stage = 0, phase = 0, iter = 0;
+    Ring ring;
+    for (;;) {
+        int4 task;
+        if (!engine::read_task(aux, w, ring, 0, false, 0, task) || task.x < 0)
+            break;
+        const Phase& f = p.ph[task.x];
+        int k0, k1;
+        part_range(f, task_part(task), k0, k1);
+        const uint32_t idesc = f.f16 ? ptx::idesc_f16_f32(BM, BN, f.a_mn, f.b_mn)
+                                     : ptx::idesc_bf16_f32(BM, BN, f.a_mn, f.b_mn);
+        // K-major: rows of 128 B, 8-row groups 1 KiB apart, a 16-deep k step
+        // advances 32 B inside the swizzle atom.  MN-major: 64-wide blocks
+        // 8 KiB apart, 8-deep k groups 1 KiB apart, a k step advances 2 KiB.
+        const uint32_t a_lbo = f.a_mn ? B_BOX_BYTES : 16, b_lbo = f.b_mn ? B_BOX_BYTES : 16;
+        const uint64_t a_step = f.a_mn ? 2048 >> 4 : 32 >> 4, b_step = f.b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint32_t acc = iter & 1u;
+        if (!wait_mbar_cl(w, ptx::smem_u32(&aux.tmem_empty[acc]), ((iter >> 1) & 1u) ^ 1u, SITE_TMEM_EMPTY))
+            break;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            ok = wait_mbar(w, ptx::smem_u32(&aux.full[stage]), phase, SITE_SMEM_FULL);
+            if (!ok)
+                break;
+            ptx::tc_fence_after();
+            const uint32_t sa = ptx::smem_u32(stages + stage * STAGE_BYTES);
+            const uint64_t adesc = ptx::sdesc_sw128(sa, a_lbo, 1024);
+            const uint64_t bdesc = ptx::sdesc_sw128(sa + A_STAGE_BYTES, b_lbo, 1024);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+                ptx::umma_bf16_pair(d_tmem, adesc + k * a_step, bdesc + k * b_step, idesc,
+                                    (kb > k0 || k > 0) ? 1u : 0u);
+            ptx::umma_commit_pair_mc(ptx::smem_u32(&aux.empty[stage]), 0x3);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok)
+            break;
+        ptx::umma_commit_pair_mc(ptx::smem_u32(&aux.tmem_full[acc]), 0x3);
+        ++iter;
+    }
+    // Exit: wait until every MMA this thread issued has completed.
+    ptx::umma_commit_pair_mc(ptx::smem_u32(&aux.drain), 0x1);
+    wait_own(w, ptx::smem_u32(&aux.drain), 0u);
+}
+
+// ----------------------------------------------------------------- epilogue
+// Where a tile's finished sums come from: this CTA's accumulator, or the K
+// parts' partial tiles in memory, added in part order.
+struct Source {
+    uint32_t taddr;          // tensor memory, this warp's lanes
+    const float4* parts;     // NULL: tensor memory; else this warp and lane's words of part 0
+    int nparts;
+};
+constexpr int PART_VEC = PART_FLOATS / 4;                    // float4 of one tile
+constexpr int PART_WARP_VEC = PART_VEC / TILE_PARTS;         // of one warp's 32 rows
+
+__device__ __forceinline__ void source32(const Source& s, int c, float (&v)[32])
+{
+    if (s.parts == nullptr) {
+        uint32_t r[32];
+        __syncwarp();
+        ptx::tmem_ld_32x32b_x32(s.taddr + c * 32, r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = __uint_as_float(r[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = 0.0f;
+    for (int q = 0; q < s.nparts; ++q) {
+        const float4* src = s.parts + static_cast<int64_t>(q) * PART_VEC + c * 8 * 32;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 x = __ldcg(src + j * 32);
+            v[4 * j] += x.x;
+            v[4 * j + 1] += x.y;
+            v[4 * j + 2] += x.z;
+            v[4 * j + 3] += x.w;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_out(bool f16, float lo, float hi)
+{
+    if (!f16)
+        return pack_bf16x2(lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The activation and its derivative at x, through the logistic function s:
+// SiLU: x s(x), s + x s (1 - s).  GELU (tanh form): x s(2u), s + x s (1 - s)
+// 2u', u = sqrt(2/pi) (x + 0.044715 x^3).  The derivative's x is kept within
+// +-30, where s (1 - s) is 0 in fp32, so that x^2 stays finite.
+template <int ACT>
+__device__ __forceinline__ void act_both(float x, float& a, float& d)
+{
+    if (ACT == TFFN_ACT_RELU) {
+        a = fmaxf(x, 0.0f);
+        d = x > 0.0f ? 1.0f : 0.0f;
+    } else if (ACT == TFFN_ACT_SILU) {
+        const float s = ptx::rcp_approx(1.0f + ex2_approx(x * -1.44269504f));
+        a = x * s;
+        d = fmaf(a, 1.0f - s, s);
+    } else if (ACT == TFFN_ACT_GELU_TANH) {
+        const float c0 = -2.3022082f, c1 = -0.10294324f;   // as act_apply
+        const float xc = fminf(fmaxf(x, -30.0f), 30.0f);
+        const float x2 = xc * xc;
+        const float s = ptx::rcp_approx(1.0f + ex2_approx(xc * fmaf(c1, x2, c0)));
+        a = x * s;
+        // 2u' = 2 sqrt(2/pi) (1 + 3 * 0.044715 x^2)
+        d = fmaf(xc * s * (1.0f - s), fmaf(0.21406443f, x2, 1.5957691f), s);
+    } else {
+        a = x;
+        d = 1.0f;
+    }
+}
+
+// 64 packed columns of this thread's row into a staging buffer and out.
+__device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage, uint32_t& sb, int lane,
+                                        const uint32_t (&lo)[16], const uint32_t (&hi)[16], int32_t x, int32_t y,
+                                        int32_t z)
+{
+    const uint32_t buf = stage + sb * OUT_BUF_BYTES;
+    out_buffer_free(lane);
+    stage_half(buf, lane, 0, lo);
+    stage_half(buf, lane, 1, hi);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_3d(map, buf, x, y, z);
+        ptx::bulk_commit_group();
+    }
+    sb ^= 1u;
+}
+
+// The same 32 rows x 64 columns transposed: row c of the box holds column c of
+// the tile, 32 values of 2 bytes.  Lane pairs swap halves so that each lane
+// writes one 32-bit word (two neighbouring rows of one column).
+__device__ __forceinline__ void put_box_t(const CUtensorMap* map, uint32_t stage, uint32_t& sb, int lane,
+                                          const uint32_t (&lo)[16], const uint32_t (&hi)[16], int32_t row,
+                                          int32_t col, int32_t z)
+{
+    const uint32_t buf = stage + sb * OUT_BUF_BYTES;
+    out_buffer_free(lane);
+    const bool odd = (lane & 1) != 0;
+    const uint32_t at = buf + static_cast<uint32_t>(odd ? 64 : 0) + static_cast<uint32_t>(lane >> 1) * 4u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t v = i < 16 ? lo[i & 15] : hi[i & 15];   // columns 2i, 2i + 1 of this row
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
+        const uint32_t u = odd ? __byte_perm(o, v, 0x7632) : __byte_perm(v, o, 0x5410);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 128u), "r"(u) : "memory");
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_3d(map, buf, row, col, z);
+        ptx::bulk_commit_group();
+    }
+    sb ^= 1u;
+}
+
+struct TileCtx {
+    int32_t row0;        // first row of this warp
+    int32_t col0;        // first column of the tile
+    int32_t nchunks;     // 32-column chunks inside the matrix
+    int32_t batch;
+    int lane;
+    uint32_t stage;      // the warp's staging buffers
+};
+
+// out = alpha D + beta C + diag I
+__device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
+                                             bool mirror, uint32_t sb)
+{
+    const float alpha = f.alpha, beta = f.beta, diag = f.diag;
+    const bool f16 = f.out_f16 != 0;
+    const int32_t row = t.row0 + t.lane;
+    const int32_t ncols = f.ncols;
+    const __half* c_row = nullptr;
+    if (f.aux0 != nullptr && row < f.rows)
+        c_row = static_cast<const __half*>(f.aux0) + t.batch * f.aux_batch + static_cast<int64_t>(row) * f.aux_ld;
+    const CUtensorMap* map = &p.map[f.out[0]];
+    const CUtensorMap* map_t = &p.map[f.out_t];
+    for (int c = 0; c < t.nchunks; c += 2) {
+        uint32_t pk[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (c + h >= t.nchunks) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    pk[h][i] = 0u;   // columns past the output: clipped by the store
+                continue;
+            }
+            const int32_t x = t.col0 + (c + h) * 32;
+            // C's rows are 16-byte aligned and padded to 8 columns.  They may
+            // have been written earlier in this launch: read past L1.
+            uint4 cv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                cv[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (c_row != nullptr && x + 8 * j < ncols)
+                    cv[j] = __ldcg(reinterpret_cast<const uint4*>(c_row + x + 8 * j));
+            }
+            float v[32];
+            source32(src, c + h, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t cw[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&cw[q]));
+                    const int i = j * 8 + q * 2;
+                    v[i] = fmaf(alpha, v[i], beta * cf.x) + (x + i == row ? diag : 0.0f);
+                    v[i + 1] = fmaf(alpha, v[i + 1], beta * cf.y) + (x + i + 1 == row ? diag : 0.0f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[h][i] = pack_out(f16, v[2 * i], v[2 * i + 1]);
+        }
+        put_box(map, t.stage, sb, t.lane, pk[0], pk[1], t.col0 + c * 32, t.row0, t.batch);
+        if (mirror)
+            put_box_t(map_t, t.stage, sb, t.lane, pk[0], pk[1], t.row0, t.col0 + c * 32, t.batch);
+    }
+    return sb;
+}
+
+// Gated tile: gate columns [0, 128) and linear columns [128, 256) of the
+// accumulator give 128 columns of G, U and H = act(G) U, H formed from the
+// fp32 sums and each rounded to bf16 once.
+template <int ACT>
+__device__ __forceinline__ uint32_t epi_glu_save(const Params& p, const Phase& f, const Source& src,
+                                                 const TileCtx& t, uint32_t sb)
+{
+    for (int c = 0; c < t.nchunks; c += 2) {
+        uint32_t g[2][16], u[2][16], hh[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (c + h >= t.nchunks) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    g[h][i] = u[h][i] = hh[h][i] = 0u;
+                continue;
+            }
+            float a[32], b[32];
+            source32(src, c + h, a);
+            source32(src, BN_CTA / 32 + c + h, b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                g[h][i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
+                u[h][i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
+                hh[h][i] = pack_bf16x2(act_apply(ACT, a[2 * i]) * b[2 * i], act_apply(ACT, a[2 * i + 1]) * b[2 * i + 1]);
+            }
+        }
+        const int32_t x = t.col0 + c * 32;
+        put_box(&p.map[f.out[2]], t.stage, sb, t.lane, hh[0], hh[1], x, t.row0, 0);
+        put_box(&p.map[f.out[0]], t.stage, sb, t.lane, g[0], g[1], x, t.row0, 0);
+        put_box(&p.map[f.out[1]], t.stage, sb, t.lane, u[0], u[1], x, t.row0, 0);
+    }
+    return sb;
+}
+
+// 32 columns (64 bytes) of this thread's row of a bf16 tensor; zeros outside.
+__device__ __forceinline__ void row32(const __nv_bfloat16* row, int32_t x, int32_t ncols, uint4 (&v)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row != nullptr && x + 8 * j < ncols)
+            v[j] = __ldg(reinterpret_cast<const uint4*>(row + x + 8 * j));
+    }
+}
+
+// D = dH: dU = dH act(G), dG = dH U act'(G), and H = act(G) U again for dW2
+// (recomputed rather than kept: the forward pass would have to write it and
+// the caller to hold it, for the same read here).
+template <int ACT>
+__device__ __forceinline__ uint32_t epi_glu_grad(const Params& p, const Phase& f, const Source& src,
+                                                 const TileCtx& t, uint32_t sb)
+{
+    const int32_t row = t.row0 + t.lane;
+    const __nv_bfloat16 *g_row = nullptr, *u_row = nullptr;
+    if (row < f.rows) {
+        g_row = static_cast<const __nv_bfloat16*>(f.aux0) + static_cast<int64_t>(row) * f.aux_ld;
+        u_row = static_cast<const __nv_bfloat16*>(f.aux1) + static_cast<int64_t>(row) * f.aux_ld;
+    }
+    const int32_t ncols = f.ncols;
+    for (int c = 0; c < t.nchunks; c += 2) {
+        uint32_t dg[2][16], du[2][16], hh[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (c + h >= t.nchunks) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    dg[h][i] = du[h][i] = hh[h][i] = 0u;
+                continue;
+            }
+            const int32_t x = t.col0 + (c + h) * 32;
+            uint4 gv[4], uv[4];
+            row32(g_row, x, ncols, gv);
+            row32(u_row, x, ncols, uv);
+            float d[32];
+            source32(src, c + h, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t gw[4] = {gv[j].x, gv[j].y, gv[j].z, gv[j].w};
+                const uint32_t uw[4] = {uv[j].x, uv[j].y, uv[j].z, uv[j].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = j * 4 + q;
+                    float a0, d0, a1, d1;
+                    act_both<ACT>(bf16_lo(gw[q]), a0, d0);
+                    act_both<ACT>(bf16_hi(gw[q]), a1, d1);
+                    const float u0 = bf16_lo(uw[q]), u1 = bf16_hi(uw[q]);
+                    dg[h][i] = pack_bf16x2(d[2 * i] * u0 * d0, d[2 * i + 1] * u1 * d1);
+                    du[h][i] = pack_bf16x2(d[2 * i] * a0, d[2 * i + 1] * a1);
+                    hh[h][i] = pack_bf16x2(a0 * u0, a1 * u1);
+                }
+            }
+        }
+        const int32_t x = t.col0 + c * 32;
+        put_box(&p.map[f.out[0]], t.stage, sb, t.lane, dg[0], dg[1], x, t.row0, 0);
+        put_box(&p.map[f.out[1]], t.stage, sb, t.lane, du[0], du[1], x, t.row0, 0);
+        put_box(&p.map[f.out[2]], t.stage, sb, t.lane, hh[0], hh[1], x, t.row0, 0);
+    }
+    return sb;
+}
+
+__device__ __noinline__ uint32_t epilogue_tile(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
+                                               bool mirror, uint32_t sb)
+{
+#define TFFN_EPI(FN)                                                                 \
+    switch (f.act) {                                                                 \
+    case TFFN_ACT_SILU: return FN<TFFN_ACT_SILU>(p, f, src, t, sb);                  \
+    case TFFN_ACT_GELU_TANH: return FN<TFFN_ACT_GELU_TANH>(p, f, src, t, sb);        \
+    case TFFN_ACT_RELU: return FN<TFFN_ACT_RELU>(p, f, src, t, sb);                  \
+    default: return FN<TFFN_ACT_NONE>(p, f, src, t, sb);                             \
+    }
+    if (f.epi == EPI_GLU_SAVE) {
+        TFFN_EPI(epi_glu_save)
+    }
+    if (f.epi == EPI_GLU_GRAD) {
+        TFFN_EPI(epi_glu_grad)
+    }
+#undef TFFN_EPI
+    return epi_poly(p, f, src, t, mirror, sb);
+}
+
+__device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank, int warp,
+                             int lane, uint32_t out_stage)
+{
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);   // TMEM lanes [32 quad, 32 quad + 32)
+    uint32_t iter = 0, sb = 0;
+    Ring ring;
+    for (;;) {
+        int4 task;
+        if (!engine::read_task(aux, w, ring, rank, true, lane, task) || task.x < 0)
+            break;
+        const Phase& f = p.ph[task.x];
+        const uint32_t acc = iter & 1u;
+        if (!wait_mbar(w, ptx::smem_u32(&aux.tmem_full[acc]), (iter >> 1) & 1u, SITE_TMEM_FULL))
+            break;
+        ptx::tc_fence_after();
+        TileCtx t;
+        const int32_t tile_cols = f.epi == EPI_GLU_SAVE ? BN_CTA : BN;
+        t.row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA + static_cast<int32_t>(quad) * 32;
+        t.col0 = task.z * tile_cols;
+        const int32_t left = f.ncols - t.col0;
+        t.nchunks = left >= tile_cols ? tile_cols / 32 : (left + 31) / 32;
+        t.batch = task_batch(task);
+        t.lane = lane;
+        t.stage = out_stage;
+        Source src;
+        src.taddr = tmem_base + ((quad * 32u) << 16) + acc * BN;
+        src.parts = nullptr;
+        src.nparts = 0;
+        const bool inside = t.row0 < f.rows;   // else nothing of this warp's rows is stored
+        bool finish = inside;
+        if (f.splits > 1) {
+            // This part's sums to memory; the last part of the tile to arrive
+            // (per warp) adds all of them, in part order.
+            const int32_t tile = (t.batch * f.m_tiles + task.y - f.m_first) * f.n_tiles + task.z;
+            float4* part = reinterpret_cast<float4*>(f.partial) + static_cast<int64_t>(tile) * f.splits * PART_VEC +
+                           (rank * EPI_WARPS + quad) * PART_WARP_VEC + lane;
+            if (inside) {
+                float4* dst = part + static_cast<int64_t>(task_part(task)) * PART_VEC;
+                const int chunks = f.epi == EPI_GLU_SAVE ? BN / 32 : t.nchunks;
+                for (int c = 0; c < chunks; ++c) {
+                    float v[32];
+                    source32(src, c, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(dst + (c * 8 + j) * 32, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t last = 0;
+                if (lane == 0) {
+                    uint32_t* ctr = p.counters + f.arrive_base + tile * TILE_PARTS + rank * EPI_WARPS + quad;
+                    last = ptx::atom_add_acq_rel_gpu(ctr, 1u) == static_cast<uint32_t>(f.splits - 1) ? 1u : 0u;
+                }
+                finish = __shfl_sync(0xffffffffu, last, 0) != 0u;
+                __threadfence();
+            } else {
+                finish = false;
+            }
+            src.parts = part;
+            src.nparts = f.splits;
+        }
+        const bool mirror = f.sym != 0 && task.y != task.z;
+        if (f.splits > 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_on_leader(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
+        }
+        if (finish)
+            sb = epilogue_tile(p, f, src, t, mirror, sb);
+        if (f.splits <= 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_on_leader(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
+        }
+        ++iter;
+        // Count this warp's part of the tile once its stores are complete.  A
+        // warp outside the matrix counts at once (with split K: in part 0).
+        if (f.done_base >= 0 && (finish || (!inside && task_part(task) == 0))) {
+            if (lane == 0) {
+                ptx::bulk_wait_group<0>();
+                ptx::fence_proxy_async_global();
+                __threadfence();
+                uint32_t* ctr = p.counters + f.done_base + t.batch * f.done_stride;
+                ptx::red_relaxed_add_gpu(ctr + 1 + task.y, 1u);
+                if (mirror)
+                    ptx::red_relaxed_add_gpu(ctr + 1 + task.z, 1u);
+                ptx::red_relaxed_add_gpu(ctr, 1u);
+            }
+            __syncwarp();
+        }
+    }
+    // Every store of this warp has completed before the CTA can leave.
+    if (lane == 0) {
+        ptx::bulk_wait_group<0>();
+        __threadfence();
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------- kernel
+__global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Aux& aux = *reinterpret_cast<Aux*>(stages + STAGES * STAGE_BYTES + OUT_BYTES);
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const uint32_t rank = ptx::cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&aux.full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&aux.empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(ptx::smem_u32(&aux.tmem_full[a]), 1);
+            ptx::mbar_init(ptx::smem_u32(&aux.tmem_empty[a]), 2 * EPI_WARPS);
+        }
+        for (int s = 0; s < TASK_SLOTS; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&aux.task_full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&aux.task_empty[s]), TASK_CONSUMERS);
+        }
+        ptx::mbar_init(ptx::smem_u32(&aux.drain), 1);
+        aux.abort = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(&aux.tmem_base), TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();   // both CTAs' barriers exist before any remote arrive
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = aux.tmem_base;
+    const WaitCtx w{&aux.abort, p.ctrl, p.wait_limit_ns, ptx::mapa(ptx::smem_u32(&aux.abort), rank ^ 1u)};
+
+    if (warp == 0) {
+        if (lane == 0)
+            run_a_loader(p, aux, stages, w, rank);
+    } else if (warp == B_LOADER_WARP) {
+        if (lane == 0)
+            run_b_loader(p, aux, stages, w, rank);
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0)
+            run_mma(p, aux, stages, w, tmem_base);
+    } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
+        run_epilogue(p, aux, w, tmem_base, rank, warp, lane,
+                     ptx::smem_u32(stages + STAGES * STAGE_BYTES) +
+                         static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES));
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    // The leader's MMAs read the peer's shared memory: neither CTA leaves (or
+    // frees its tensor memory) before both are done.
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+    // The last CTA out leaves the ticket and the counters at zero.
+    __shared__ uint32_t last_out;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last_out = atomicAdd(&p.ctrl->done, 1u) == gridDim.x - 1 ? 1u : 0u;
+    }
+    __syncthreads();
+    if (last_out != 0u) {
+        __threadfence();
+        for (int i = threadIdx.x; i < p.n_counters; i += NUM_THREADS)
+            p.counters[i] = 0u;
+        if (threadIdx.x == 0) {
+            p.ctrl->ticket = 0u;
+            p.ctrl->done = 0u;
+        }
+    }
+}
+
+}  // namespace phases
+}  // namespace tffn

@@ -1,0 +1,84 @@
+// phases_params.cuh -- the parameter block of the phase kernel (phases.cuh),
+// filled by the host (train.cu).
+#pragma once
+
+#include "engine.cuh"
+
+namespace tffn {
+namespace phases {
+
+using engine::BK;
+using engine::BM;
+using engine::BN;
+using engine::BN_CTA;
+using engine::EPI_WARPS;
+
+constexpr int MAX_MAPS = 24;
+constexpr int MAX_PHASES = 24;
+constexpr int TILE_PARTS = 2 * EPI_WARPS;              // epilogue warps that finish one tile
+constexpr int PART_FLOATS = BM * BN;                   // fp32 partial sums of one split tile
+enum Epilogue : int32_t {
+    EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16, read where it lies)
+    EPI_GLU_SAVE = 1,   // 128 columns of G and of U: out = {G, U, act(G) U}
+    EPI_GLU_GRAD = 2,   // D = dH: out = {dG, dU, H} from the saved G, U
+};
+
+enum DepMode : int32_t { DEP_NONE = 0, DEP_BAND = 1, DEP_ALL = 2 };
+
+// What an operand's loads wait for: `base` is the first counter of the phase
+// that wrote it (its batch stride in `stride`), DEP_BAND waits for the band of
+// this tile (row tile for A, column tile for B).
+struct Dep {
+    int32_t mode;
+    int32_t base;
+    int32_t stride;
+    int32_t target_band;
+    int32_t target_all;
+};
+
+struct Phase {
+    int32_t first;              // first ticket
+    int32_t m_first;            // first row tile
+    int32_t m_tiles, n_tiles;   // row tiles and column tiles of one batch entry
+    int32_t batches;
+    int32_t splits;             // K parts per tile
+    int32_t sym;                // lower triangle only (m_tiles == n_tiles), mirrored
+    int32_t group_m;            // row tiles per raster group
+    int32_t nk[2];              // 64-deep k-blocks of the two K segments
+    int8_t map_a[2], map_b[2];  // maps of the segments (GLU_SAVE: map_b = {W1, W3}, one segment)
+    int8_t a_mn, b_mn;          // 1: MN-major operand
+    int8_t a4, b4;              // MN-major operand through one 4-D copy (else two 3-D boxes)
+    int8_t f16;                 // operand type: 1 fp16, 0 bf16
+    int8_t out_f16;             // output type
+    int8_t out[3];              // output maps
+    int8_t out_t;               // map of the mirrored store (sym)
+    int32_t epi;                // Epilogue
+    int32_t act;
+    int32_t rows, ncols;        // output extent of one batch entry
+    float alpha, beta, diag;
+    const void* aux0;           // GLU_GRAD: G, bf16; POLY: C, fp16 (nullable)
+    const void* aux1;           // GLU_GRAD: U
+    int64_t aux_ld;             // row stride of the aux tensors
+    int64_t aux_batch;          // batch stride
+    Dep dep_a, dep_b;
+    int32_t done_base;          // counters this phase adds to: [batch][1 + bands]; -1: none
+    int32_t done_stride;        // 1 + bands
+    int32_t arrive_base;        // split arrival counters: [tile][TILE_PARTS]
+    int32_t pad_;
+    float* partial;             // split partial tiles
+};
+
+struct Params {
+    CUtensorMap map[MAX_MAPS];
+    Phase ph[MAX_PHASES];
+    int32_t n_phases;
+    int32_t total;              // tickets
+    DevCtrl* ctrl;
+    uint32_t* counters;         // zero when a launch starts, zeroed again by the last CTA out
+    int32_t n_counters;
+    int32_t pad_;
+    uint64_t wait_limit_ns;
+};
+
+}  // namespace phases
+}  // namespace tffn

@@ -1,0 +1,761 @@
+// train.cu -- the C ABI of the training operators (include/tffn.h): argument
+// validation, tensor maps and the phase tables of the gated FFN's forward and
+// backward passes and of the Newton-Schulz steps; layer norm's entry points.
+// All arithmetic happens in the kernels (phases.cuh, norm.cu, muon.cu).
+#include <algorithm>
+#include <cstring>
+#include <memory>
+#include <new>
+
+#include "../../include/tffn.h"
+#include "api.h"
+#include "launch.h"
+#include "phases_params.cuh"
+#include "train.h"
+
+namespace {
+
+using namespace tffn;
+using phases::Dep;
+using phases::Phase;
+using PhaseParams = phases::Params;
+
+constexpr int64_t BM = phases::BM, BN = phases::BN, BK = phases::BK;
+constexpr int64_t MAX_DIM = int64_t(1) << 31;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t pad_to(int64_t a, int64_t b) { return div_up(a, b) * b; }
+
+// A matrix stack of 16-bit values: `rows` x `cols` per batch entry, row stride
+// `ld` and batch stride `bs` in elements.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+    int64_t batch = 1, bs = 0;
+    bool f16 = false;
+};
+
+Mat dense(const void* p, int64_t rows, int64_t cols) { return Mat{p, rows, cols, cols}; }
+
+// Collects the tensor maps of one launch.
+struct Maps {
+    PhaseParams& p;
+    int n = 0;
+    bool failed = false;
+
+    int add(int rank, const Mat& m, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+            CUtensorMapSwizzle sw)
+    {
+        if (n >= phases::MAX_MAPS ||
+            api_encode(&p.map[n], m.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                       m.p, dims, strides, box, sw) != 0) {
+            failed = true;
+            return 0;
+        }
+        return n++;
+    }
+    static cuuint64_t batch_bytes(const Mat& m) { return static_cast<cuuint64_t>(m.batch > 1 ? m.bs : m.ld) * 2; }
+    int box3(const Mat& m, uint32_t bx, uint32_t by, CUtensorMapSwizzle sw)
+    {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                                    static_cast<cuuint64_t>(m.batch)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(m.ld) * 2, batch_bytes(m)};
+        const cuuint32_t box[3] = {bx, by, 1};
+        return add(3, m, dims, strides, box, sw);
+    }
+    // An operand whose columns are the reduction index: 64 of them x 128 rows.
+    int k_major(const Mat& m) { return box3(m, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B); }
+    // An operand whose rows are the reduction index: 64 of them x 128 columns,
+    // in one copy when the columns come in whole blocks of 64.
+    static bool four(const Mat& m) { return m.cols % 64 == 0; }
+    int mn_major(const Mat& m)
+    {
+        if (!four(m))
+            return box3(m, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(m.rows), static_cast<cuuint64_t>(m.cols / 64),
+                                    static_cast<cuuint64_t>(m.batch)};
+        const cuuint64_t strides[3] = {static_cast<cuuint64_t>(m.ld) * 2, 128, batch_bytes(m)};
+        const cuuint32_t box[4] = {64, 64, 2, 1};
+        return add(4, m, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    int out(const Mat& m) { return box3(m, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B); }
+    int out_t(const Mat& m) { return box3(m, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE); }
+};
+
+// A phase D [rows x ncols] = A B with K = nk0 (+ nk1) k-blocks.
+Phase make_phase(int64_t rows, int64_t ncols, int64_t tile_cols, int64_t k0, int64_t k1, int64_t raster_k)
+{
+    Phase f;
+    std::memset(&f, 0, sizeof(f));
+    f.m_tiles = static_cast<int32_t>(div_up(rows, BM));
+    f.n_tiles = static_cast<int32_t>(div_up(ncols, tile_cols));
+    f.batches = 1;
+    f.splits = 1;
+    // row tiles per raster group, as the FFN engine: about 38 MB of operand
+    // panels in flight
+    f.group_m = raster_k >= 8192 ? 8 : 4;
+    f.nk[0] = static_cast<int32_t>(div_up(k0, BK));
+    f.nk[1] = static_cast<int32_t>(div_up(k1, BK));
+    f.rows = static_cast<int32_t>(rows);
+    f.ncols = static_cast<int32_t>(ncols);
+    f.alpha = 1.0f;
+    f.done_base = -1;
+    return f;
+}
+
+int64_t phase_tiles(const Phase& f)
+{
+    return (f.sym ? int64_t(f.m_tiles) * (f.m_tiles + 1) / 2 : int64_t(f.m_tiles) * f.n_tiles) * f.batches;
+}
+
+// K parts of a phase with fewer tiles than CTA pairs: as many as fill the
+// pairs, none shorter than eight k-blocks (a part's fp32 sums cost a write and
+// a read of the tile).
+int split_parts(int64_t tiles, int64_t nk, int64_t pairs)
+{
+    const int64_t s = std::min<int64_t>(std::min<int64_t>(pairs / std::max<int64_t>(tiles, 1), nk / 8), 16);
+    return s < 2 ? 1 : static_cast<int>(s);
+}
+
+// The launch's table: tickets and counters are handed out in the order of add().
+struct Table {
+    PhaseParams& p;
+    int64_t tickets = 0;
+    int64_t counters = 0;
+
+    // counters a phase adds to when its tiles are stored
+    void count_done(Phase& f, int64_t bands)
+    {
+        f.done_base = static_cast<int32_t>(counters);
+        f.done_stride = static_cast<int32_t>(1 + bands);
+        counters += (1 + bands) * f.batches;
+    }
+    void split(Phase& f, int parts, float* partial)
+    {
+        f.splits = parts;
+        f.partial = partial;
+        f.arrive_base = static_cast<int32_t>(counters);
+        if (parts > 1)
+            counters += int64_t(f.m_tiles) * f.n_tiles * f.batches * phases::TILE_PARTS;
+    }
+    void add(const Phase& f)
+    {
+        Phase& q = p.ph[p.n_phases++];
+        q = f;
+        q.first = static_cast<int32_t>(tickets);
+        tickets += phase_tiles(f) * f.splits;
+    }
+};
+
+// A wait on the phase (or groups of one phase) that counted into `by`.
+// tiles_band: its tiles per 256-row band of output; all: its tiles per batch entry.
+Dep depend(int mode, const Phase& by, int64_t tiles_band, int64_t all)
+{
+    Dep d;
+    d.mode = mode;
+    d.base = by.done_base;
+    d.stride = by.done_stride;
+    d.target_band = static_cast<int32_t>(tiles_band * phases::TILE_PARTS);
+    d.target_all = static_cast<int32_t>(all * phases::TILE_PARTS);
+    return d;
+}
+
+int launch_table(PhaseParams& p, Table& t, const ApiSpace& ws, cudaStream_t s)
+{
+    if (t.tickets >= MAX_DIM || t.counters > static_cast<int64_t>(ws.counter_words))
+        return TFFN_ERR_UNSUPPORTED;
+    p.total = static_cast<int32_t>(t.tickets);
+    p.n_counters = static_cast<int32_t>(t.counters);
+    p.ctrl = ws.ctrl;
+    p.counters = ws.counters;
+    p.wait_limit_ns = option_wait_limit_ns();
+    return launch_phases(p, s) == 0 ? TFFN_OK : TFFN_ERR_CUDA;
+}
+
+// ------------------------------------------------------------- gated FFN
+// Bytes of fp32 partial tiles: at most one tile per CTA pair and phase.
+size_t partial_bytes(int sms) { return size_t(sms / 2 + 1) * phases::PART_FLOATS * 4; }
+
+struct GluSpace {
+    size_t dg, du, h, part, total;   // offsets into the workspace's data
+};
+
+GluSpace glu_space(int64_t M, int64_t O, int sms, bool backward)
+{
+    GluSpace g;
+    const size_t mat = static_cast<size_t>(pad_to(M * O * 2, 256));
+    g.h = 0;
+    g.dg = mat;
+    g.du = 2 * mat;
+    g.part = (backward ? 3 : 1) * mat;
+    g.total = g.part + partial_bytes(sms);
+    return g;
+}
+
+bool dim_ok(int64_t d) { return d >= 8 && d % 8 == 0 && d < MAX_DIM; }
+bool act_ok(int a)
+{
+    return a == TFFN_ACT_NONE || a == TFFN_ACT_RELU || a == TFFN_ACT_GELU_TANH || a == TFFN_ACT_SILU;
+}
+
+// Splits `bands` row bands into at most `most` groups of whole raster groups.
+int64_t band_group(int64_t bands, int64_t raster, int64_t most) { return pad_to(div_up(bands, most), raster); }
+
+// Adds `up` and `down` (down's A bands wait for up's) band group by band
+// group: up(0), up(1), down(0), up(2), down(1), ..., so that down's tiles run
+// while up's are still being produced and read them from L2.
+void add_interleaved(Table& t, const Phase& up, const Phase& down, int64_t bands, int64_t group)
+{
+    const int64_t ng = div_up(bands, group);
+    auto part = [&](const Phase& f, int64_t g) {
+        Phase q = f;
+        q.m_first = static_cast<int32_t>(g * group);
+        q.m_tiles = static_cast<int32_t>(std::min(group, bands - g * group));
+        t.add(q);
+    };
+    for (int64_t g = 0; g <= ng; ++g) {
+        if (g < ng)
+            part(up, g);
+        if (g >= 1)
+            part(down, g - 1);
+    }
+}
+
+constexpr int64_t MAX_GROUPS = 8;
+static_assert(2 * MAX_GROUPS + 3 <= phases::MAX_PHASES, "phase table");
+
+int glu_train_forward(const void* X, const void* W1, const void* W3, const void* W2, int act, int64_t M, int64_t N,
+                      int64_t O, int64_t P, void* Y, void* G, void* U, cudaStream_t s)
+{
+    std::lock_guard<std::mutex> lock(api_mutex());
+    int sms = 0;
+    int rc = api_sms(&sms);
+    if (rc != TFFN_OK)
+        return rc;
+    const GluSpace gs = glu_space(M, O, sms, false);
+    ApiSpace ws;
+    rc = api_space(gs.total, s, &ws);
+    if (rc != TFFN_OK)
+        return rc;
+    const int pairs = phase_pairs();
+    if (pairs < 1)
+        return TFFN_ERR_CUDA;
+    std::unique_ptr<PhaseParams> pp(new (std::nothrow) PhaseParams);
+    if (!pp)
+        return TFFN_ERR_CUDA;
+    std::memset(static_cast<void*>(pp.get()), 0, sizeof(PhaseParams));
+    PhaseParams& p = *pp;
+    Maps mp{p};
+    Table t{p};
+    const int64_t bands = div_up(M, BM);
+    const Mat x = dense(X, M, N), w1 = dense(W1, N, O), w3 = dense(W3, N, O), w2 = dense(W2, O, P);
+    const Mat h = dense(ws.data + gs.h, M, O);
+
+    Phase up = make_phase(M, O, phases::BN_CTA, N, 0, N);
+    up.epi = phases::EPI_GLU_SAVE;
+    up.act = act;
+    up.map_a[0] = static_cast<int8_t>(mp.k_major(x));
+    up.map_b[0] = static_cast<int8_t>(mp.mn_major(w1));
+    up.map_b[1] = static_cast<int8_t>(mp.mn_major(w3));
+    up.b_mn = 1;
+    up.b4 = Maps::four(w1);
+    up.out[0] = static_cast<int8_t>(mp.out(dense(G, M, O)));
+    up.out[1] = static_cast<int8_t>(mp.out(dense(U, M, O)));
+    up.out[2] = static_cast<int8_t>(mp.out(h));
+    t.count_done(up, bands);
+
+    Phase down = make_phase(M, P, BN, O, 0, N);
+    down.map_a[0] = static_cast<int8_t>(mp.k_major(h));
+    down.map_b[0] = static_cast<int8_t>(mp.mn_major(w2));
+    down.b_mn = 1;
+    down.b4 = Maps::four(w2);
+    down.out[0] = static_cast<int8_t>(mp.out(dense(Y, M, P)));
+    down.dep_a = depend(phases::DEP_BAND, up, up.n_tiles, phase_tiles(up));
+    if (mp.failed)
+        return TFFN_ERR_INVALID_ARG;
+    const int parts = split_parts(phase_tiles(down), down.nk[0], pairs);
+    t.split(down, parts, reinterpret_cast<float*>(ws.data + gs.part));
+    add_interleaved(t, up, down, bands, parts > 1 ? bands : band_group(bands, up.group_m, MAX_GROUPS));
+    api_timing_start(s);
+    rc = launch_table(p, t, ws, s);
+    api_timing_stop(s);
+    if (rc == TFFN_OK)
+        api_launches(1);
+    return rc;
+}
+
+int glu_backward(const void* dY, const void* X, const void* W1, const void* W3, const void* W2, const void* G,
+                 const void* U, int act, int64_t M, int64_t N, int64_t O, int64_t P, void* dX, void* dW1, void* dW3,
+                 void* dW2, cudaStream_t s)
+{
+    std::lock_guard<std::mutex> lock(api_mutex());
+    int sms = 0;
+    int rc = api_sms(&sms);
+    if (rc != TFFN_OK)
+        return rc;
+    const GluSpace gs = glu_space(M, O, sms, true);
+    ApiSpace ws;
+    rc = api_space(gs.total, s, &ws);
+    if (rc != TFFN_OK)
+        return rc;
+    const int pairs = phase_pairs();
+    if (pairs < 1)
+        return TFFN_ERR_CUDA;
+    std::unique_ptr<PhaseParams> pp(new (std::nothrow) PhaseParams);
+    if (!pp)
+        return TFFN_ERR_CUDA;
+    std::memset(static_cast<void*>(pp.get()), 0, sizeof(PhaseParams));
+    PhaseParams& p = *pp;
+    Maps mp{p};
+    Table t{p};
+    const int64_t bands = div_up(M, BM);
+    const Mat dy = dense(dY, M, P), x = dense(X, M, N), w1 = dense(W1, N, O), w3 = dense(W3, N, O),
+              w2 = dense(W2, O, P);
+    const Mat dg = dense(ws.data + gs.dg, M, O), du = dense(ws.data + gs.du, M, O), h = dense(ws.data + gs.h, M, O);
+
+    // dH = dY W2^T, and from it dG, dU and H
+    Phase up = make_phase(M, O, BN, P, 0, P);
+    up.epi = phases::EPI_GLU_GRAD;
+    up.act = act;
+    up.map_a[0] = static_cast<int8_t>(mp.k_major(dy));
+    up.map_b[0] = static_cast<int8_t>(mp.k_major(w2));
+    up.out[0] = static_cast<int8_t>(mp.out(dg));
+    up.out[1] = static_cast<int8_t>(mp.out(du));
+    up.out[2] = static_cast<int8_t>(mp.out(h));
+    up.aux0 = G;
+    up.aux1 = U;
+    up.aux_ld = O;
+    t.count_done(up, bands);
+    const int64_t up_tiles = phase_tiles(up);
+
+    // dX = dG W1^T + dU W3^T, one accumulation over both
+    Phase down = make_phase(M, N, BN, O, O, P);
+    down.map_a[0] = static_cast<int8_t>(mp.k_major(dg));
+    down.map_a[1] = static_cast<int8_t>(mp.k_major(du));
+    down.map_b[0] = static_cast<int8_t>(mp.k_major(w1));
+    down.map_b[1] = static_cast<int8_t>(mp.k_major(w3));
+    down.out[0] = static_cast<int8_t>(mp.out(dense(dX, M, N)));
+    down.dep_a = depend(phases::DEP_BAND, up, up.n_tiles, up_tiles);
+
+    // dW = A^T B over the rows of A and B
+    auto weight = [&](const Mat& a, const Mat& b, void* out, bool a_made, bool b_made) {
+        Phase f = make_phase(a.cols, b.cols, BN, M, 0, M);
+        f.a_mn = f.b_mn = 1;
+        f.a4 = Maps::four(a);
+        f.b4 = Maps::four(b);
+        f.map_a[0] = static_cast<int8_t>(mp.mn_major(a));
+        f.map_b[0] = static_cast<int8_t>(mp.mn_major(b));
+        f.out[0] = static_cast<int8_t>(mp.out(dense(out, a.cols, b.cols)));
+        if (a_made)
+            f.dep_a = depend(phases::DEP_ALL, up, up.n_tiles, up_tiles);
+        if (b_made)
+            f.dep_b = depend(phases::DEP_ALL, up, up.n_tiles, up_tiles);
+        return f;
+    };
+    const Phase f2 = weight(h, dy, dW2, true, false);
+    const Phase f1 = weight(x, dg, dW1, false, true);
+    const Phase f3 = weight(x, du, dW3, false, true);
+    if (mp.failed)
+        return TFFN_ERR_INVALID_ARG;
+    const int parts = split_parts(phase_tiles(down), down.nk[0] + down.nk[1], pairs);
+    t.split(down, parts, reinterpret_cast<float*>(ws.data + gs.part));
+    add_interleaved(t, up, down, bands, parts > 1 ? bands : band_group(bands, up.group_m, MAX_GROUPS));
+    t.add(f2);
+    t.add(f1);
+    t.add(f3);
+    api_timing_start(s);
+    rc = launch_table(p, t, ws, s);
+    api_timing_stop(s);
+    if (rc == TFFN_OK)
+        api_launches(1);
+    return rc;
+}
+
+// ------------------------------------------------------- orthogonalisation
+constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f, NS_EPS = 1e-7f;
+// X is kept 64 times its value, so that entries of a normalised large matrix
+// (1 / sqrt(m n)) stay clear of fp16's subnormals; its norm is at most ~1.2.
+constexpr float NS_SCALE = 64.0f;
+constexpr int STEPS_PER_LAUNCH = 5;
+// Largest side (its band counters fit a launch) and largest stack.
+constexpr int64_t MUON_MAX_DIM = int64_t(1) << 18, MUON_MAX_BATCH = 65535;
+static_assert(3 * STEPS_PER_LAUNCH <= phases::MAX_PHASES, "phase table");
+
+struct MuonSpace {
+    int64_t side, ldx, lds;    // smaller side; row strides of X and of A, B
+    int64_t per_launch;        // batch entries per launch
+    size_t x0, x1, a, b, part, norm, total;
+};
+
+MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
+{
+    MuonSpace q;
+    q.side = std::min(m, n);
+    q.ldx = pad_to(n, 64);
+    q.lds = pad_to(q.side, 8);
+    // counters of a launch: per step and entry the bands of A, of B and of X;
+    // beside them the arrivals of split products (fewer tiles than CTA pairs,
+    // so under 10,000 words)
+    const int64_t nb = div_up(q.side, BM), mb = div_up(m, BM);
+    const int64_t words = STEPS_PER_LAUNCH * (2 * (1 + nb) + 1 + mb);
+    q.per_launch = std::max<int64_t>(1, std::min<int64_t>(batch, 50000 / words));
+    size_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t at = o;
+        o += static_cast<size_t>(pad_to(bytes, 256));
+        return at;
+    };
+    q.x0 = take(batch * m * q.ldx * 2);
+    q.x1 = take(batch * m * q.ldx * 2);
+    q.a = take(q.per_launch * q.side * q.lds * 2);
+    q.b = take(q.per_launch * q.side * q.lds * 2);
+    q.part = take(static_cast<int64_t>(2 * partial_bytes(sms)));
+    q.norm = take(batch * muon_norm_blocks(m * n, sms) * 8);
+    q.total = o;
+    return q;
+}
+
+// Steps [0, steps) of entries [first, first + count) from X0; the last one
+// stores bf16 into `out`.  X alternates between the two buffers.
+int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, int64_t first, int64_t count, int steps,
+                int& cur, bool last, const Mat& out, int pairs, cudaStream_t s)
+{
+    std::unique_ptr<PhaseParams> pp(new (std::nothrow) PhaseParams);
+    if (!pp)
+        return TFFN_ERR_CUDA;
+    std::memset(static_cast<void*>(pp.get()), 0, sizeof(PhaseParams));
+    PhaseParams& p = *pp;
+    Maps mp{p};
+    Table t{p};
+    const bool tall = m > n;
+    const int64_t side = q.side;
+    const int64_t x_bytes = m * q.ldx * 2;
+    Mat x[2];
+    for (int i = 0; i < 2; ++i) {
+        x[i] = Mat{ws.data + (i ? q.x1 : q.x0) + first * x_bytes, m, q.ldx, q.ldx, count, m * q.ldx, true};
+    }
+    const Mat A{ws.data + q.a, side, side, q.lds, count, side * q.lds, true};
+    const Mat B{ws.data + q.b, side, side, q.lds, count, side * q.lds, true};
+    const int xk[2] = {mp.k_major(x[0]), mp.k_major(x[1])};
+    const int xm[2] = {mp.mn_major(x[0]), mp.mn_major(x[1])};
+    const int xo[2] = {mp.out(x[0]), mp.out(x[1])};
+    const int ak = mp.k_major(A), ao = mp.out(A), at = mp.out_t(A);
+    const int bk = mp.k_major(B), bo = mp.out(B), bt = mp.out_t(B);
+    const int oo = last ? mp.out(out) : 0;
+    if (mp.failed)
+        return TFFN_ERR_INVALID_ARG;
+    float* partial = reinterpret_cast<float*>(ws.data + q.part);
+    const int64_t sb = div_up(side, BM);
+
+    Phase prev;   // the update that made the current X
+    bool has_prev = false;
+    for (int i = 0; i < steps; ++i) {
+        // A = X X^T (tall: X^T X) / 64^2
+        Phase gram = make_phase(side, side, BN, tall ? m : n, 0, tall ? m : n);
+        gram.batches = static_cast<int32_t>(count);
+        gram.sym = 1;
+        gram.f16 = gram.out_f16 = 1;
+        gram.a_mn = gram.b_mn = gram.a4 = gram.b4 = tall ? 1 : 0;
+        gram.map_a[0] = gram.map_b[0] = static_cast<int8_t>(tall ? xm[cur] : xk[cur]);
+        gram.alpha = 1.0f / (NS_SCALE * NS_SCALE);
+        gram.out[0] = static_cast<int8_t>(ao);
+        gram.out_t = static_cast<int8_t>(at);
+        if (has_prev) {
+            gram.dep_a = gram.dep_b = depend(tall ? phases::DEP_ALL : phases::DEP_BAND, prev, prev.n_tiles,
+                                             int64_t(prev.m_tiles) * prev.n_tiles);
+        }
+        t.count_done(gram, sb);
+        t.split(gram, split_parts(phase_tiles(gram), gram.nk[0], pairs), partial);
+        t.add(gram);
+
+        // B = a I + b A + c A A
+        Phase sq = make_phase(side, side, BN, side, 0, side);
+        sq.batches = static_cast<int32_t>(count);
+        sq.sym = 1;
+        sq.f16 = sq.out_f16 = 1;
+        sq.map_a[0] = sq.map_b[0] = static_cast<int8_t>(ak);
+        sq.alpha = NS_C;
+        sq.beta = NS_B;
+        sq.diag = NS_A;
+        sq.aux0 = A.p;
+        sq.aux_ld = q.lds;
+        sq.aux_batch = A.bs;
+        sq.out[0] = static_cast<int8_t>(bo);
+        sq.out_t = static_cast<int8_t>(bt);
+        sq.dep_a = sq.dep_b = depend(phases::DEP_BAND, gram, sb, sb * (sb + 1) / 2);
+        t.count_done(sq, sb);
+        t.split(sq, 1, partial);
+        t.add(sq);
+
+        // X <- B X (tall: X B)
+        const bool end = last && i + 1 == steps;
+        Phase up = make_phase(m, end ? n : q.ldx, BN, side, 0, side);
+        up.batches = static_cast<int32_t>(count);
+        up.f16 = 1;
+        up.out_f16 = end ? 0 : 1;
+        up.alpha = end ? 1.0f / NS_SCALE : 1.0f;
+        up.out[0] = static_cast<int8_t>(end ? oo : xo[cur ^ 1]);
+        const Dep on_b = depend(phases::DEP_BAND, sq, sb, sb * (sb + 1) / 2);
+        Dep on_x;
+        std::memset(&on_x, 0, sizeof(on_x));
+        if (has_prev)
+            on_x = depend(tall ? phases::DEP_BAND : phases::DEP_ALL, prev, prev.n_tiles,
+                          int64_t(prev.m_tiles) * prev.n_tiles);
+        if (tall) {
+            up.map_a[0] = static_cast<int8_t>(xk[cur]);
+            up.map_b[0] = static_cast<int8_t>(bk);
+            up.dep_a = on_x;
+            up.dep_b = on_b;
+        } else {
+            up.map_a[0] = static_cast<int8_t>(bk);
+            up.map_b[0] = static_cast<int8_t>(xm[cur]);
+            up.b_mn = up.b4 = 1;
+            up.dep_a = on_b;
+            up.dep_b = on_x;
+        }
+        t.count_done(up, up.m_tiles);
+        t.split(up, 1, partial);
+        t.add(up);
+        prev = up;
+        has_prev = true;
+        cur ^= 1;
+    }
+    return launch_table(p, t, ws, s);
+}
+
+int muon_run(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int steps, void* out, cudaStream_t s)
+{
+    std::lock_guard<std::mutex> lock(api_mutex());
+    int sms = 0;
+    int rc = api_sms(&sms);
+    if (rc != TFFN_OK)
+        return rc;
+    const MuonSpace q = muon_space(batch, m, n, sms);
+    ApiSpace ws;
+    rc = api_space(q.total, s, &ws);
+    if (rc != TFFN_OK)
+        return rc;
+    const int pairs = phase_pairs();
+    if (pairs < 1)
+        return TFFN_ERR_CUDA;
+    const bool f32 = dtype == TFFN_F32;
+    double* part = reinterpret_cast<double*>(ws.data + q.norm);
+    const int blocks = muon_norm_blocks(m * n, sms);
+    int launches = 2;
+    if (launch_muon_norm(G, f32, batch, m * n, part, blocks, s) != 0 ||
+        launch_muon_pack(G, f32, batch, m, n, part, blocks, NS_SCALE, NS_EPS, ws.data + q.x0, q.ldx, sms, s) != 0)
+        return TFFN_ERR_CUDA;
+    // rows of the result that TMA can store where they belong, else through X's buffer
+    const bool direct = n % 8 == 0 && aligned(out, 16);
+    int end = 0;
+    api_timing_start(s);
+    for (int64_t e = 0; e < batch; e += q.per_launch) {
+        const int64_t count = std::min(q.per_launch, batch - e);
+        int cur = 0;
+        for (int done = 0; done < steps;) {
+            const int k = std::min(STEPS_PER_LAUNCH, steps - done);
+            Mat dst;
+            if (direct)
+                dst = Mat{static_cast<uint8_t*>(out) + e * m * n * 2, m, n, n, count, m * n, false};
+            else {
+                const int buf = (cur ^ (k & 1));   // the buffer that the last step would write
+                dst = Mat{ws.data + (buf ? q.x1 : q.x0) + e * m * q.ldx * 2, m, n, q.ldx, count, m * q.ldx, false};
+                end = buf;
+            }
+            rc = muon_launch(ws, q, m, n, e, count, k, cur, done + k == steps, dst, pairs, s);
+            if (rc != TFFN_OK)
+                return rc;
+            done += k;
+            ++launches;
+        }
+    }
+    api_timing_stop(s);
+    if (!direct) {
+        if (launch_muon_unpack(ws.data + (end ? q.x1 : q.x0), batch, m, n, q.ldx, out, sms, s) != 0)
+            return TFFN_ERR_CUDA;
+        ++launches;
+    }
+    api_launches(launches);
+    return TFFN_OK;
+}
+
+bool dtype_ok(int d) { return d == TFFN_BF16 || d == TFFN_F32; }
+size_t dtype_size(int d) { return d == TFFN_F32 ? 4 : 2; }
+
+}  // namespace
+
+// ====================================================================== ABI
+
+extern "C" {
+
+int ffn_glu_forward_train(const void* X, const void* W1, const void* W3, const void* W2, int act, int64_t M,
+                          int64_t N, int64_t O, int64_t P, void* Y, void* G, void* U, struct CUstream_st* stream)
+{
+    api_launches(0);
+    if (M < 0 || M >= MAX_DIM || !dim_ok(N) || !dim_ok(O) || !dim_ok(P) || !act_ok(act))
+        return TFFN_ERR_INVALID_ARG;
+    if (M == 0)
+        return TFFN_OK;   // empty call: X, Y, G and U may be NULL
+    for (const void* q : {X, W1, W3, W2, static_cast<const void*>(Y), static_cast<const void*>(G),
+                          static_cast<const void*>(U)})
+        if (!q || !aligned(q, 16))
+            return TFFN_ERR_INVALID_ARG;
+    return glu_train_forward(X, W1, W3, W2, act, M, N, O, P, Y, G, U, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ffn_glu_backward(const void* dY, const void* X, const void* W1, const void* W3, const void* W2, const void* G,
+                     const void* U, int act, int64_t M, int64_t N, int64_t O, int64_t P, void* dX, void* dW1,
+                     void* dW3, void* dW2, struct CUstream_st* stream)
+{
+    api_launches(0);
+    if (M < 0 || M >= MAX_DIM || !dim_ok(N) || !dim_ok(O) || !dim_ok(P) || !act_ok(act))
+        return TFFN_ERR_INVALID_ARG;
+    for (const void* q : {static_cast<const void*>(dW1), static_cast<const void*>(dW3), static_cast<const void*>(dW2)})
+        if (!q || !aligned(q, 16))
+            return TFFN_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {   // no rows: the weights' gradients are zero
+        if (cudaMemsetAsync(dW1, 0, static_cast<size_t>(N) * O * 2, s) != cudaSuccess ||
+            cudaMemsetAsync(dW3, 0, static_cast<size_t>(N) * O * 2, s) != cudaSuccess ||
+            cudaMemsetAsync(dW2, 0, static_cast<size_t>(O) * P * 2, s) != cudaSuccess)
+            return TFFN_ERR_CUDA;
+        return TFFN_OK;
+    }
+    for (const void* q : {dY, X, W1, W3, W2, G, U, static_cast<const void*>(dX)})
+        if (!q || !aligned(q, 16))
+            return TFFN_ERR_INVALID_ARG;
+    return glu_backward(dY, X, W1, W3, W2, G, U, act, M, N, O, P, dX, dW1, dW3, dW2, s);
+}
+
+size_t ffn_glu_train_workspace_bytes(int64_t M, int64_t O)
+{
+    if (M < 0 || M >= MAX_DIM || !dim_ok(O))
+        return 0;
+    int sms = 1024;   // without a device: planned for up to 1024 SMs
+    {
+        std::lock_guard<std::mutex> lock(api_mutex());
+        int d = 0;
+        if (api_sms(&d) == TFFN_OK)
+            sms = d;
+    }
+    return api_sync_bytes() + glu_space(M, O, sms, true).total;
+}
+
+int layer_norm_forward(const void* X, const void* R, const void* gamma, const void* beta, float eps, int dtype,
+                       int param_dtype, int64_t T, int64_t N, void* Y, void* S, float* mean, float* rstd,
+                       struct CUstream_st* stream)
+{
+    api_launches(0);
+    if (T < 0 || T >= MAX_DIM || N < 1 || N >= MAX_DIM || !dtype_ok(dtype) || !dtype_ok(param_dtype) || !(eps >= 0.0f))
+        return TFFN_ERR_INVALID_ARG;
+    if (T == 0)
+        return TFFN_OK;
+    if (!X || !Y || !mean || !rstd || (R && !S))
+        return TFFN_ERR_INVALID_ARG;
+    for (const void* q : {X, R, static_cast<const void*>(Y), static_cast<const void*>(S)})
+        if (!aligned(q, dtype_size(dtype)))
+            return TFFN_ERR_INVALID_ARG;
+    if (!aligned(gamma, dtype_size(param_dtype)) || !aligned(beta, dtype_size(param_dtype)) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return TFFN_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    int sms = 0;
+    const int rc = api_sms(&sms);
+    if (rc != TFFN_OK)
+        return rc;
+    const NormFwd a{X, R, gamma, beta, Y, S, mean, rstd, T, N, eps, dtype == TFFN_F32, param_dtype == TFFN_F32};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    api_timing_start(s);
+    if (launch_norm_fwd(a, sms, s) != 0)
+        return TFFN_ERR_CUDA;
+    api_timing_stop(s);
+    api_launches(1);
+    return TFFN_OK;
+}
+
+int layer_norm_backward(const void* dY, const void* S, const void* gamma, const float* mean, const float* rstd,
+                        const void* dS, int dtype, int param_dtype, int64_t T, int64_t N, void* dX, float* dgamma,
+                        float* dbeta, struct CUstream_st* stream)
+{
+    api_launches(0);
+    if (T < 0 || T >= MAX_DIM || N < 1 || N >= MAX_DIM || !dtype_ok(dtype) || !dtype_ok(param_dtype) ||
+        (dgamma == nullptr) != (dbeta == nullptr) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
+        return TFFN_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) {   // no rows: the parameters' gradients are zero
+        if (dgamma && (cudaMemsetAsync(dgamma, 0, static_cast<size_t>(N) * 4, s) != cudaSuccess ||
+                       cudaMemsetAsync(dbeta, 0, static_cast<size_t>(N) * 4, s) != cudaSuccess))
+            return TFFN_ERR_CUDA;
+        return TFFN_OK;
+    }
+    if (!dY || !S || !mean || !rstd || !dX)
+        return TFFN_ERR_INVALID_ARG;
+    for (const void* q : {dY, S, dS, static_cast<const void*>(dX)})
+        if (!aligned(q, dtype_size(dtype)))
+            return TFFN_ERR_INVALID_ARG;
+    if (!aligned(gamma, dtype_size(param_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return TFFN_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    int sms = 0;
+    int rc = api_sms(&sms);
+    if (rc != TFFN_OK)
+        return rc;
+    ApiSpace ws;
+    rc = api_space(static_cast<size_t>(norm_bwd_ctas(T, N, sms)) * 2 * N * 4, s, &ws);
+    if (rc != TFFN_OK)
+        return rc;
+    const NormBwd a{dY, S, gamma, dS, mean, rstd, dX, dgamma, dbeta, reinterpret_cast<float*>(ws.data),
+                    T,  N, dtype == TFFN_F32, param_dtype == TFFN_F32};
+    api_timing_start(s);
+    const int n = launch_norm_bwd(a, sms, s);
+    if (n < 0)
+        return TFFN_ERR_CUDA;
+    api_timing_stop(s);
+    api_launches(n);
+    return TFFN_OK;
+}
+
+size_t layer_norm_workspace_bytes(int64_t T, int64_t N)
+{
+    if (T < 0 || T >= MAX_DIM || N < 1 || N >= MAX_DIM)
+        return 0;
+    int sms = 1024;
+    {
+        std::lock_guard<std::mutex> lock(api_mutex());
+        int d = 0;
+        if (api_sms(&d) == TFFN_OK)
+            sms = d;
+    }
+    return api_sync_bytes() + static_cast<size_t>(norm_bwd_ctas(T, N, sms)) * 2 * N * 4;
+}
+
+int muon_orthogonalize(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int steps, void* out,
+                       struct CUstream_st* stream)
+{
+    api_launches(0);
+    if (batch < 0 || m < 0 || n < 0 || m > MUON_MAX_DIM || n > MUON_MAX_DIM || batch > MUON_MAX_BATCH ||
+        steps < 1 || steps > 64 || !dtype_ok(dtype))
+        return TFFN_ERR_INVALID_ARG;
+    if (batch == 0 || m == 0 || n == 0)
+        return TFFN_OK;
+    if (!G || !out || !aligned(G, dtype_size(dtype)) || !aligned(out, 2))
+        return TFFN_ERR_INVALID_ARG;
+    return muon_run(G, dtype, batch, m, n, steps, out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t muon_workspace_bytes(int64_t batch, int64_t m, int64_t n)
+{
+    if (batch < 0 || m < 1 || n < 1 || m > MUON_MAX_DIM || n > MUON_MAX_DIM || batch > MUON_MAX_BATCH)
+        return 0;
+    int sms = 1024;
+    {
+        std::lock_guard<std::mutex> lock(api_mutex());
+        int d = 0;
+        if (api_sms(&d) == TFFN_OK)
+            sms = d;
+    }
+    return api_sync_bytes() + muon_space(batch, m, n, sms).total;
+}
+
+}  // extern "C"

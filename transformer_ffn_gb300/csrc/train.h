@@ -1,0 +1,50 @@
+// train.h -- host-side launchers of the training operators' kernels.  Every
+// launcher returns 0 or -1 (launch error; the CUDA error is left to the caller).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace tffn {
+namespace phases {
+struct Params;
+}
+
+// CTA pairs of the phase kernel that are resident at once (-1: CUDA error).
+int phase_pairs();
+int launch_phases(const phases::Params& p, cudaStream_t s);
+
+// Layer norm (norm.cu).  f32 / p32: activations / parameters are fp32, else bf16.
+struct NormFwd {
+    const void *X, *R, *gamma, *beta;   // R, gamma, beta nullable
+    void *Y, *S;                        // S: written only with R
+    float *mean, *rstd;
+    int64_t T, N;
+    float eps;
+    bool f32, p32;
+};
+struct NormBwd {
+    const void *dY, *S, *gamma, *dS;    // gamma, dS nullable
+    const float *mean, *rstd;
+    void* dX;
+    float *dgamma, *dbeta;              // nullable together
+    float* partial;                     // [norm_bwd_ctas][2][N]
+    int64_t T, N;
+    bool f32, p32;
+};
+int launch_norm_fwd(const NormFwd& a, int sms, cudaStream_t s);
+// CTAs that accumulate column sums of a [T x N] backward pass.
+int norm_bwd_ctas(int64_t T, int64_t N, int sms);
+// Kernels launched, or -1.
+int launch_norm_bwd(const NormBwd& a, int sms, cudaStream_t s);
+
+// Newton-Schulz (muon.cu): sums of squares, the scaled fp16 copy X [B][m][ld],
+// and the dense copy of a padded result.
+int muon_norm_blocks(int64_t elems, int sms);
+int launch_muon_norm(const void* G, bool f32, int64_t batch, int64_t elems, double* part, int blocks, cudaStream_t s);
+int launch_muon_pack(const void* G, bool f32, int64_t batch, int64_t m, int64_t n, const double* part, int blocks,
+                     float scale, float eps, void* X, int64_t ld, int sms, cudaStream_t s);
+int launch_muon_unpack(const void* X, int64_t batch, int64_t m, int64_t n, int64_t ld, void* out, int sms,
+                       cudaStream_t s);
+
+}  // namespace tffn
