@@ -285,7 +285,19 @@ def moe_glu_forward(X, gate_logits, top_k, W1, W3, W2, act="silu", out=None, rou
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+_BF16, _F32 = torch.bfloat16, torch.float32
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+def _is(t, dtype, shape, device):
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous())
+
+
 def _check_tensor(name, t, dtype, shape, device):
+    if _is(t, dtype, shape, device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -294,12 +306,11 @@ def _check_tensor(name, t, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _check_lead(name, t, dims, dtypes):
-    """The tensor that fixes a call's device and types."""
+    """The tensor that fixes a call's device and types; returns its device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -308,33 +319,40 @@ def _check_lead(name, t, dims, dtypes):
         raise ValueError(f"{name} must have {' or '.join(str(d) for d in dims)} dimensions")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
+    dev = t.device
+    if dev.type != "cuda" or dev.index != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, is on {dev}")
+    return dev
 
 
-class _OnStream:
-    """A call's stream: results are allocated on it, and torch is told that it
-    uses the operands, so that their memory is not handed out too early."""
+def _stream_of(stream, dev, operands):
+    """The call's raw stream.  On a stream other than the current one torch is
+    told that it uses the operands, so that their memory is not handed out too
+    early."""
+    raw = _current_stream(dev.index)
+    if stream is None or stream.cuda_stream == raw:
+        return raw
+    for t in operands:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
-    def __init__(self, stream, *operands):
-        self.stream = stream
-        if stream is not None and stream != torch.cuda.current_stream():
-            for t in operands:
-                if t is not None:
-                    t.record_stream(stream)
-        else:
-            self.stream = None
-        self.ptr = _stream_ptr(stream)
 
-    def empty(self, shape, dtype, device):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+def _alloc(stream, dev, *specs):
+    """Result tensors (shape, dtype), allocated on the call's stream."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_norm_param(name, t, N, dev):
-    _check_tensor(name, t, t.dtype if getattr(t, "dtype", None) in _DTYPES else torch.float32, (N,), dev)
+    _check_tensor(name, t, t.dtype if getattr(t, "dtype", None) in _DTYPES else _F32, (N,), dev)
+    return t.dtype
 
 
 def layer_norm_forward(X, gamma, beta, residual=None, eps=1e-5, stream=None):
@@ -342,27 +360,28 @@ def layer_norm_forward(X, gamma, beta, residual=None, eps=1e-5, stream=None):
     * rstd * gamma + beta over the rows of S [T, N].  X, residual, Y and S are
     bfloat16 or float32; gamma and beta [N] are bfloat16 or float32, or None;
     mean and rstd [T] are float32."""
-    L = load()
-    _check_lead("X", X, (2,), (torch.bfloat16, torch.float32))
-    dev = X.device
-    T, N = X.shape
-    par = gamma if gamma is not None else beta
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _check_norm_param(name, t, N, dev)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta must have the same type")
+    L = _lib or load()
+    dev = _check_lead("X", X, (2,), _DTYPES)
+    dtype, shape = X.dtype, X.shape
+    T, N = shape
+    par = _F32
+    if beta is not None:
+        par = _check_norm_param("beta", beta, N, dev)
+    if gamma is not None:
+        if _check_norm_param("gamma", gamma, N, dev) is not par and beta is not None:
+            raise TypeError("gamma and beta must have the same type")
+        par = gamma.dtype
     if residual is not None:
-        _check_tensor("residual", residual, X.dtype, X.shape, dev)
-    on = _OnStream(stream, X, residual, gamma, beta)
-    Y = on.empty((T, N), X.dtype, dev)
-    S = X if residual is None else on.empty((T, N), X.dtype, dev)
-    stats = on.empty((2, T), torch.float32, dev)
-    mean, rstd = stats[0], stats[1]
-    rc = L.layer_norm_forward(_ptr(X), _ptr(residual), _ptr(gamma), _ptr(beta), float(eps), _DTYPES[X.dtype],
-                              _DTYPES[par.dtype] if par is not None else 0, T, N, _ptr(Y),
-                              _ptr(S) if residual is not None else None, _ptr(mean), _ptr(rstd), on.ptr)
-    _raise(rc, "layer_norm_forward")
+        _check_tensor("residual", residual, dtype, shape, dev)
+    s = _stream_of(stream, dev, (X, residual, gamma, beta))
+    Y, stats, *rest = _alloc(stream, dev, (shape, dtype), ((2, T), _F32), *(() if residual is None else ((shape, dtype),)))
+    mean, rstd = stats.unbind(0)
+    at = stats.data_ptr()
+    S = rest[0] if rest else X
+    rc = L.layer_norm_forward(X.data_ptr(), _addr(residual), _addr(gamma), _addr(beta), eps, _DTYPES[dtype],
+                              _DTYPES[par], T, N, Y.data_ptr(), S.data_ptr() if rest else None, at, at + 4 * T, s)
+    if rc:
+        _raise(rc, "layer_norm_forward")
     return Y, S, mean, rstd
 
 
@@ -370,83 +389,84 @@ def layer_norm_backward(dY, S, gamma, mean, rstd, dS=None, weight_grads=True, st
     """(dX, dgamma, dbeta) of layer_norm_forward: dX is the gradient of X (and of
     the residual), with dS, the gradient that reaches S past the norm, added;
     dgamma and dbeta are float32 (None without weight_grads)."""
-    L = load()
-    _check_lead("dY", dY, (2,), (torch.bfloat16, torch.float32))
-    dev = dY.device
-    T, N = dY.shape
-    _check_tensor("S", S, dY.dtype, dY.shape, dev)
-    if gamma is not None:
-        _check_norm_param("gamma", gamma, N, dev)
-    _check_tensor("mean", mean, torch.float32, (T,), dev)
-    _check_tensor("rstd", rstd, torch.float32, (T,), dev)
+    L = _lib or load()
+    dev = _check_lead("dY", dY, (2,), _DTYPES)
+    dtype, shape = dY.dtype, dY.shape
+    T, N = shape
+    _check_tensor("S", S, dtype, shape, dev)
+    par = _F32 if gamma is None else _check_norm_param("gamma", gamma, N, dev)
+    _check_tensor("mean", mean, _F32, (T,), dev)
+    _check_tensor("rstd", rstd, _F32, (T,), dev)
     if dS is not None:
-        _check_tensor("dS", dS, dY.dtype, dY.shape, dev)
-    on = _OnStream(stream, dY, S, gamma, mean, rstd, dS)
-    dX = on.empty((T, N), dY.dtype, dev)
-    dgamma = dbeta = None
-    if weight_grads:
-        dgamma, dbeta = on.empty((N,), torch.float32, dev), on.empty((N,), torch.float32, dev)
-    rc = L.layer_norm_backward(_ptr(dY), _ptr(S), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dS), _DTYPES[dY.dtype],
-                               _DTYPES[gamma.dtype] if gamma is not None else 0, T, N, _ptr(dX), _ptr(dgamma),
-                               _ptr(dbeta), on.ptr)
-    _raise(rc, "layer_norm_backward")
+        _check_tensor("dS", dS, dtype, shape, dev)
+    s = _stream_of(stream, dev, (dY, S, gamma, mean, rstd, dS))
+    dX, *grads = _alloc(stream, dev, (shape, dtype), *(((N,), _F32), ((N,), _F32)) if weight_grads else ())
+    dgamma, dbeta = grads if weight_grads else (None, None)
+    rc = L.layer_norm_backward(dY.data_ptr(), S.data_ptr(), _addr(gamma), mean.data_ptr(), rstd.data_ptr(),
+                               _addr(dS), _DTYPES[dtype], _DTYPES[par], T, N, dX.data_ptr(), _addr(dgamma),
+                               _addr(dbeta), s)
+    if rc:
+        _raise(rc, "layer_norm_backward")
     return dX, dgamma, dbeta
 
 
-def _check_glu_weights(X, W1, W3, W2):
-    dev, bf = X.device, torch.bfloat16
-    N = X.shape[1]
+def _check_glu(X, W1, W3, W2):
+    """(device, M, N, O, P) of a gated FFN's operands."""
+    dev = _check_lead("X", X, (2,), (_BF16,))
+    M, N = X.shape
     if not isinstance(W1, torch.Tensor) or W1.dim() != 2 or not isinstance(W2, torch.Tensor) or W2.dim() != 2:
         raise ValueError("W1 and W2 must be 2-dimensional tensors")
     O, P = W1.shape[1], W2.shape[1]
-    for name, t, shape in (("W1", W1, (N, O)), ("W3", W3, (N, O)), ("W2", W2, (O, P))):
-        _check_tensor(name, t, bf, shape, dev)
-    return N, O, P
+    _check_tensor("W1", W1, _BF16, (N, O), dev)
+    _check_tensor("W3", W3, _BF16, (N, O), dev)
+    _check_tensor("W2", W2, _BF16, (O, P), dev)
+    return dev, M, N, O, P
 
 
 def ffn_glu_forward_train(X, W1, W3, W2, act="silu", stream=None):
     """(Y, G, U): the gated FFN Y = (act(G) * U) @ W2 with G = X @ W1 and U = X @ W3
     kept for ffn_glu_backward; all bfloat16."""
-    L = load()
-    _check_lead("X", X, (2,), (torch.bfloat16,))
-    N, O, P = _check_glu_weights(X, W1, W3, W2)
-    M = X.shape[0]
-    on = _OnStream(stream, X, W1, W3, W2)
-    Y, G, U = (on.empty((M, c), torch.bfloat16, X.device) for c in (P, O, O))
-    rc = L.ffn_glu_forward_train(_ptr(X), _ptr(W1), _ptr(W3), _ptr(W2), _act(act), M, N, O, P, _ptr(Y), _ptr(G),
-                                 _ptr(U), on.ptr)
-    _raise(rc, "ffn_glu_forward_train")
+    L = _lib or load()
+    dev, M, N, O, P = _check_glu(X, W1, W3, W2)
+    s = _stream_of(stream, dev, (X, W1, W3, W2))
+    Y, G, U = _alloc(stream, dev, ((M, P), _BF16), ((M, O), _BF16), ((M, O), _BF16))
+    rc = L.ffn_glu_forward_train(X.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), _act(act), M, N, O, P,
+                                 Y.data_ptr(), G.data_ptr(), U.data_ptr(), s)
+    if rc:
+        _raise(rc, "ffn_glu_forward_train")
     return Y, G, U
 
 
 def ffn_glu_backward(dY, X, W1, W3, W2, G, U, act="silu", stream=None):
     """(dX, dW1, dW3, dW2), all bfloat16: the gradients of ffn_glu_forward_train from
     Y's gradient, the forward pass's operands and its G and U."""
-    L = load()
-    _check_lead("X", X, (2,), (torch.bfloat16,))
-    N, O, P = _check_glu_weights(X, W1, W3, W2)
-    M, dev, bf = X.shape[0], X.device, torch.bfloat16
-    for name, t, cols in (("dY", dY, P), ("G", G, O), ("U", U, O)):
-        _check_tensor(name, t, bf, (M, cols), dev)
-    on = _OnStream(stream, dY, X, W1, W3, W2, G, U)
-    dX, dW1, dW3, dW2 = (on.empty(shape, bf, dev) for shape in ((M, N), (N, O), (N, O), (O, P)))
-    rc = L.ffn_glu_backward(_ptr(dY), _ptr(X), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(G), _ptr(U), _act(act), M, N, O, P,
-                            _ptr(dX), _ptr(dW1), _ptr(dW3), _ptr(dW2), on.ptr)
-    _raise(rc, "ffn_glu_backward")
+    L = _lib or load()
+    dev, M, N, O, P = _check_glu(X, W1, W3, W2)
+    _check_tensor("dY", dY, _BF16, (M, P), dev)
+    _check_tensor("G", G, _BF16, (M, O), dev)
+    _check_tensor("U", U, _BF16, (M, O), dev)
+    s = _stream_of(stream, dev, (dY, X, W1, W3, W2, G, U))
+    dX, dW1, dW3, dW2 = _alloc(stream, dev, ((M, N), _BF16), ((N, O), _BF16), ((N, O), _BF16), ((O, P), _BF16))
+    rc = L.ffn_glu_backward(dY.data_ptr(), X.data_ptr(), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), G.data_ptr(),
+                            U.data_ptr(), _act(act), M, N, O, P, dX.data_ptr(), dW1.data_ptr(), dW3.data_ptr(),
+                            dW2.data_ptr(), s)
+    if rc:
+        _raise(rc, "ffn_glu_backward")
     return dX, dW1, dW3, dW2
 
 
 def muon_orthogonalize(G, steps=5, stream=None):
     """The Muon optimiser's Newton-Schulz orthogonalisation of a matrix [m, n] or a
     stack of matrices [batch, m, n] (bfloat16 or float32), in bfloat16."""
-    L = load()
-    _check_lead("G", G, (2, 3), (torch.bfloat16, torch.float32))
-    m, n = G.shape[-2:]
-    on = _OnStream(stream, G)
-    out = on.empty(G.shape, torch.bfloat16, G.device)
-    rc = L.muon_orthogonalize(_ptr(G), _DTYPES[G.dtype], G.shape[0] if G.dim() == 3 else 1, m, n, int(steps),
-                              _ptr(out), on.ptr)
-    _raise(rc, "muon_orthogonalize")
+    L = _lib or load()
+    dev = _check_lead("G", G, (2, 3), _DTYPES)
+    shape = G.shape
+    s = _stream_of(stream, dev, (G,))
+    out, = _alloc(stream, dev, (shape, _BF16))
+    rc = L.muon_orthogonalize(G.data_ptr(), _DTYPES[G.dtype], shape[0] if len(shape) == 3 else 1, shape[-2],
+                              shape[-1], int(steps), out.data_ptr(), s)
+    if rc:
+        _raise(rc, "muon_orthogonalize")
     return out
 
 

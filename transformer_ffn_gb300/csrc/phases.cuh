@@ -2,8 +2,9 @@
 // matrix products in one launch: the gated FFN's training forward and backward
 // passes and the Newton-Schulz steps of muon_orthogonalize.
 //
-// A phase is D = A B over 256 x 256 output tiles with fp32 accumulation in
-// tensor memory.  Either operand may be stored with its reduction index
+// A phase is D = A B over output tiles of 256 rows x TN columns (256, or 128
+// where there are too few tiles of 256 to occupy the GPU) with fp32 accumulation
+// in tensor memory.  Either operand may be stored with its reduction index
 // contiguous (K-major) or with its row / column index contiguous (MN-major), so
 // the products with transposed operands of a backward pass read the caller's
 // row-major tensors where they lie; nothing is transposed in memory.  A phase
@@ -17,10 +18,13 @@
 // counts: per 256-row band of its output, or all of it.  Every wait points to
 // smaller tickets, so the launch finishes with any number of resident CTAs.
 //
-// Roles, tiles, rings and tensor-memory accumulators are those of the FFN
-// engine (engine.cuh): clusters of two CTAs, six 32 KiB stages per CTA, an A
-// loader that claims tickets one task ahead, a B loader, one MMA thread, four
-// epilogue warps with two 4 KiB staging buffers each.
+// The main loop is the FFN engine's (engine.cuh): clusters of two CTAs, a ring
+// of 192 KiB of stages per CTA, an A loader that claims tickets one task ahead,
+// a B loader, one MMA thread.  The epilogue has eight warps, two per tensor
+// memory lane quadrant and so two per scheduler, each taking half of the
+// tile's columns, 32 at a time, through two 2 KiB staging buffers: a tile's
+// epilogue is bound by instructions and latency, not by memory, and its time is
+// what a chain of small dependent products waits for.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -32,31 +36,35 @@ namespace tffn {
 namespace phases {
 
 using engine::A_STAGE_BYTES;
-using engine::arrive_on_leader;
 using engine::AUX_BYTES;
 using engine::B_BOX_BYTES;
-using engine::B_LOADER_WARP;
 using engine::BM_CTA;
-using engine::NUM_THREADS;
-using engine::OUT_BUF_BYTES;
-using engine::OUT_BYTES;
 using engine::out_buffer_free;
-using engine::out_store_box;
 using engine::Ring;
-using engine::STAGE_BYTES;
-using engine::stage_half;
-using engine::STAGES;
-using engine::TASK_CONSUMERS;
 using engine::TASK_SLOTS;
 using engine::TMEM_COLS;
 using engine::wait_own;
 
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + AUX_BYTES + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+constexpr int B_LOADER_WARP = 2 + EPI_WARPS;
+constexpr int NUM_THREADS = 32 * (3 + EPI_WARPS);
+constexpr uint32_t TASK_CONSUMERS = 1 + 1 + EPI_WARPS + 1 + 1 + EPI_WARPS;   // as engine::TASK_CONSUMERS
+constexpr int OUT_BUF_BYTES = 32 * 32 * 2;                 // 32 rows x 32 columns
+constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;   // 32 KiB
 
+template <int TN>
+struct Geo {
+    static constexpr int STAGE_BYTES = A_STAGE_BYTES + TN / 2 * BK * 2;
+    static constexpr int STAGES = TN == 256 ? 6 : 8;       // 192 KiB either way
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + AUX_BYTES + 1024;
+    static constexpr int PART_VEC = BM * TN / 4;           // float4 of one K part of a tile
+    static constexpr int PART_WARP_VEC = PART_VEC / TILE_PARTS;
+};
+static_assert(Geo<256>::SMEM_BYTES <= 232448 && Geo<128>::SMEM_BYTES <= 232448, "shared memory per CTA");
+
+template <int TN>
 struct Aux {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+    uint64_t full[Geo<TN>::STAGES];
+    uint64_t empty[Geo<TN>::STAGES];
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];
     uint64_t task_full[TASK_SLOTS];
@@ -66,13 +74,14 @@ struct Aux {
     uint32_t tmem_base;
     uint32_t abort;
 };
-static_assert(sizeof(Aux) <= AUX_BYTES, "aux block fits");
+static_assert(sizeof(Aux<128>) <= AUX_BYTES, "aux block fits");
 
 // A task: x = phase (-1: no more work), y = row tile, z = column tile,
 // w = batch * 256 + K part.
 __device__ __forceinline__ int task_batch(const int4& t) { return t.w >> 8; }
 __device__ __forceinline__ int task_part(const int4& t) { return t.w & 255; }
 
+template <int TN>
 __device__ __forceinline__ int4 decode_ticket(const Params& p, int32_t t)
 {
     if (t >= p.total)
@@ -87,7 +96,8 @@ __device__ __forceinline__ int4 decode_ticket(const Params& p, int32_t t)
         part = i % f.splits;
         i /= f.splits;
     }
-    const int32_t tiles = f.sym ? f.m_tiles * (f.m_tiles + 1) / 2 : f.m_tiles * f.n_tiles;
+    constexpr int SUB = BM / TN;   // column tiles per row band
+    const int32_t tiles = f.sym ? f.m_tiles * (f.m_tiles + 1) / 2 * SUB : f.m_tiles * f.n_tiles;
     int32_t batch = 0;
     if (f.batches > 1) {
         batch = i / tiles;
@@ -95,13 +105,15 @@ __device__ __forceinline__ int4 decode_ticket(const Params& p, int32_t t)
     }
     int32_t m, n;
     if (f.sym) {
+        const int32_t sub = i % SUB;
+        i /= SUB;
         // row m of the triangle starts at m (m + 1) / 2
         m = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
         while (m * (m + 1) / 2 > i)
             --m;
         while ((m + 1) * (m + 2) / 2 <= i)
             ++m;
-        n = i - m * (m + 1) / 2;
+        n = (i - m * (m + 1) / 2) * SUB + sub;
     } else {
         const int32_t per = f.group_m * f.n_tiles;
         const int32_t g = i / per;
@@ -161,7 +173,8 @@ __device__ __forceinline__ bool wait_dep(const Params& p, const WaitCtx& w, cons
     return true;
 }
 
-// One operand's 128 rows (columns) x 64 k of a stage.
+// One operand's MN rows (columns) x 64 k of a stage.
+template <int MN>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t fb, int32_t k, int32_t mn,
                                              int32_t z, bool mn_major, bool four)
 {
@@ -170,24 +183,67 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
     } else if (four) {
         ptx::tma_load_4d_pair(dst, map, fb, 0, k, mn / 64, z);
     } else {
-        ptx::tma_load_3d_pair(dst, map, fb, mn, k, z);
-        ptx::tma_load_3d_pair(dst + B_BOX_BYTES, map, fb, mn + 64, k, z);
+#pragma unroll
+        for (int i = 0; i < MN / 64; ++i)
+            ptx::tma_load_3d_pair(dst + i * B_BOX_BYTES, map, fb, mn + i * 64, k, z);
     }
 }
 
-// ----------------------------------------------------------------- loaders
-// A loader of one CTA; the leader's also claims the tickets (one task ahead,
-// so the hand-over of the next task never waits for the claim).
-__device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+// Arrive on the leader's copy of a barrier that only counts readers: the reads
+// it reports (a task slot, tensor memory) have returned their values before, so
+// the arrival needs no release, which from the peer CTA waits for the thread's
+// earlier memory operations for about a microsecond.
+__device__ __forceinline__ void arrive_read(uint32_t bar, uint32_t rank)
 {
+    if (rank == 0)
+        ptx::mbar_arrive(bar);
+    else
+        ptx::mbar_arrive_cluster_relaxed(ptx::mapa(bar, 0));
+}
+
+// The next task from this CTA's ring, its slot freed on the leader.
+template <class AuxT>
+__device__ __forceinline__ bool next_task(AuxT& aux, const WaitCtx& w, Ring& r, uint32_t rank, bool warp_wide, int lane,
+                                          int4& task)
+{
+    if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_full[r.slot]), r.phase, SITE_TASK_FULL))
+        return false;
+    const uint32_t at = ptx::smem_u32(&aux.task[r.slot]);
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(task.x), "=r"(task.y), "=r"(task.z), "=r"(task.w)
+                 : "r"(at)
+                 : "memory");
+    if (warp_wide)
+        __syncwarp();
+    // task.x == INT_MIN never: the arrival depends on the loaded value
+    if (task.x != INT32_MIN && (!warp_wide || lane == 0))
+        arrive_read(ptx::smem_u32(&aux.task_empty[r.slot]), rank);
+    r.advance();
+    return true;
+}
+
+// ----------------------------------------------------------------- loaders
+// A loader of one CTA; the leader's also claims the tickets (the next task is
+// published one task ahead, so its hand-over never waits for the claim).  A
+// pair holds two tickets beyond the one it runs, all larger, so the smallest
+// unfinished ticket is always some pair's current task.
+template <int TN>
+__device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+{
+    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0;
     int32_t known = -1;
     Ring ring;
     int32_t last_phase[STAGES];
     for (int s = 0; s < STAGES; ++s)
         last_phase[s] = -1;
+    // The ticket after the published one is already requested: its atomic's
+    // round trip passes behind a task's copies.
+    uint32_t ticket = rank == 0 ? atomicAdd(&p.ctrl->ticket, 1u) : 0u;
     auto claim_publish = [&](int4& out) -> bool {
-        out = decode_ticket(p, static_cast<int32_t>(atomicAdd(&p.ctrl->ticket, 1u)));
+        out = decode_ticket<TN>(p, static_cast<int32_t>(ticket));
+        if (out.x >= 0)
+            ticket = atomicAdd(&p.ctrl->ticket, 1u);
         if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_empty[ring.slot]), ring.phase ^ 1u, SITE_TASK_EMPTY))
             return false;
         engine::publish_task(aux, ring, out);
@@ -201,7 +257,7 @@ __device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const W
             task = ahead;
             if (task.x >= 0 && !claim_publish(ahead))
                 break;
-        } else if (!engine::read_task(aux, w, ring, rank, false, 0, task)) {
+        } else if (!next_task(aux, w, ring, rank, false, 0, task)) {
             break;
         }
         if (task.x < 0)
@@ -227,7 +283,7 @@ __device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const W
             if (rank == 0)
                 ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
             const bool second = kb >= nk0;
-            load_operand(ptx::smem_u32(stages + stage * STAGE_BYTES), second ? map1 : map0, fb,
+            load_operand<BM_CTA>(ptx::smem_u32(stages + stage * STAGE_BYTES), second ? map1 : map0, fb,
                          (second ? kb - nk0 : kb) * BK, row0, batch, mn, four);
             last_phase[stage] = static_cast<int32_t>(phase);
             if (++stage == STAGES) {
@@ -247,35 +303,37 @@ __device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const W
                 wait_own(w, ptx::smem_u32(&aux.full[s]), static_cast<uint32_t>(last_phase[s]));
 }
 
-__device__ void run_b_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+template <int TN>
+__device__ void run_b_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
 {
+    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0;
     int32_t known = -1;
     Ring ring;
     for (;;) {
         int4 task;
-        if (!engine::read_task(aux, w, ring, rank, false, 0, task) || task.x < 0)
+        if (!next_task(aux, w, ring, rank, false, 0, task) || task.x < 0)
             break;
         const Phase& f = p.ph[task.x];
         const int32_t batch = task_batch(task);
-        // A gated tile pairs 128 columns of W1 (the leader's half) with the
-        // same 128 columns of W3 (the peer's half).
+        // A gated tile pairs TN / 2 columns of W1 (the leader's half) with the
+        // same columns of W3 (the peer's half).
         const bool gated = f.epi == EPI_GLU_SAVE;
-        const int32_t col0 = gated ? task.z * BN_CTA : task.z * BN + static_cast<int32_t>(rank) * BN_CTA;
+        const int32_t col0 = gated ? task.z * (TN / 2) : task.z * TN + static_cast<int32_t>(rank) * (TN / 2);
         const CUtensorMap* map0 = &p.map[f.map_b[gated ? rank : 0]];
         const CUtensorMap* map1 = &p.map[f.map_b[1]];
         const bool mn = f.b_mn != 0, four = f.b4 != 0;
         const int nk0 = f.nk[0];
         int k0, k1;
         part_range(f, task_part(task), k0, k1);
-        if (!wait_dep(p, w, f.dep_b, batch, task.z, known))
+        if (!wait_dep(p, w, f.dep_b, batch, task.z * TN / BM, known))
             return;
         for (int kb = k0; kb < k1; ++kb) {
             if (!wait_mbar(w, ptx::smem_u32(&aux.empty[stage]), phase ^ 1u, SITE_SMEM_EMPTY))
                 return;
             const uint32_t fb = ptx::mapa(ptx::smem_u32(&aux.full[stage]), 0);
             const bool second = kb >= nk0;
-            load_operand(ptx::smem_u32(stages + stage * STAGE_BYTES) + A_STAGE_BYTES, second ? map1 : map0, fb,
+            load_operand<TN / 2>(ptx::smem_u32(stages + stage * STAGE_BYTES) + A_STAGE_BYTES, second ? map1 : map0, fb,
                          (second ? kb - nk0 : kb) * BK, col0, batch, mn, four);
             if (++stage == STAGES) {
                 stage = 0;
@@ -286,19 +344,21 @@ __device__ void run_b_loader(const Params& p, Aux& aux, uint8_t* stages, const W
 }
 
 // ------------------------------------------------------------- leader: MMA
-__device__ void run_mma(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t tmem_base)
+template <int TN>
+__device__ void run_mma(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t tmem_base)
 {
+    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0, iter = 0;
     Ring ring;
     for (;;) {
         int4 task;
-        if (!engine::read_task(aux, w, ring, 0, false, 0, task) || task.x < 0)
+        if (!next_task(aux, w, ring, 0, false, 0, task) || task.x < 0)
             break;
         const Phase& f = p.ph[task.x];
         int k0, k1;
         part_range(f, task_part(task), k0, k1);
-        const uint32_t idesc = f.f16 ? ptx::idesc_f16_f32(BM, BN, f.a_mn, f.b_mn)
-                                     : ptx::idesc_bf16_f32(BM, BN, f.a_mn, f.b_mn);
+        const uint32_t idesc = f.f16 ? ptx::idesc_f16_f32(BM, TN, f.a_mn, f.b_mn)
+                                     : ptx::idesc_bf16_f32(BM, TN, f.a_mn, f.b_mn);
         // K-major: rows of 128 B, 8-row groups 1 KiB apart, a 16-deep k step
         // advances 32 B inside the swizzle atom.  MN-major: 64-wide blocks
         // 8 KiB apart, 8-deep k groups 1 KiB apart, a k step advances 2 KiB.
@@ -308,7 +368,7 @@ __device__ void run_mma(const Params& p, Aux& aux, uint8_t* stages, const WaitCt
         if (!wait_mbar_cl(w, ptx::smem_u32(&aux.tmem_empty[acc]), ((iter >> 1) & 1u) ^ 1u, SITE_TMEM_EMPTY))
             break;
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
+        const uint32_t d_tmem = tmem_base + acc * TN;
         bool ok = true;
         for (int kb = k0; kb < k1; ++kb) {
             ok = wait_mbar(w, ptx::smem_u32(&aux.full[stage]), phase, SITE_SMEM_FULL);
@@ -339,41 +399,53 @@ __device__ void run_mma(const Params& p, Aux& aux, uint8_t* stages, const WaitCt
 }
 
 // ----------------------------------------------------------------- epilogue
-// Where a tile's finished sums come from: this CTA's accumulator, or the K
-// parts' partial tiles in memory, added in part order.
+// Where a warp's finished sums come from: its lanes and columns of the
+// accumulator, or the K parts' partial tiles in memory, added in part order.
 struct Source {
-    uint32_t taddr;          // tensor memory, this warp's lanes
+    uint32_t taddr;          // tensor memory
     const float4* parts;     // NULL: tensor memory; else this warp and lane's words of part 0
     int nparts;
+    int part_vec;            // float4 from one part to the next
 };
-constexpr int PART_VEC = PART_FLOATS / 4;                    // float4 of one tile
-constexpr int PART_WARP_VEC = PART_VEC / TILE_PARTS;         // of one warp's 32 rows
 
-__device__ __forceinline__ void source32(const Source& s, int c, float (&v)[32])
+// 32 columns: the accumulator's from column `col`, or the parts' chunk `c`.
+__device__ __forceinline__ void source32(const Source& s, int col, int c, float (&v)[32])
 {
     if (s.parts == nullptr) {
         uint32_t r[32];
         __syncwarp();
-        ptx::tmem_ld_32x32b_x32(s.taddr + c * 32, r);
+        ptx::tmem_ld_32x32b_x32(s.taddr + col, r);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             v[i] = __uint_as_float(r[i]);
         return;
     }
+    const float4* src = s.parts + c * 8 * 32;
+    float4 x[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = 0.0f;
-    for (int q = 0; q < s.nparts; ++q) {
-        const float4* src = s.parts + static_cast<int64_t>(q) * PART_VEC + c * 8 * 32;
+    for (int j = 0; j < 8; ++j)
+        x[j] = __ldcg(src + j * 32);
+    for (int q = 1; q < s.nparts; ++q) {
+        src += s.part_vec;
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            y[j] = __ldcg(src + j * 32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float4 x = __ldcg(src + j * 32);
-            v[4 * j] += x.x;
-            v[4 * j + 1] += x.y;
-            v[4 * j + 2] += x.z;
-            v[4 * j + 3] += x.w;
+            x[j].x += y[j].x;
+            x[j].y += y[j].y;
+            x[j].z += y[j].z;
+            x[j].w += y[j].w;
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[4 * j] = x[j].x;
+        v[4 * j + 1] = x[j].y;
+        v[4 * j + 2] = x[j].z;
+        v[4 * j + 3] = x[j].w;
     }
 }
 
@@ -413,61 +485,68 @@ __device__ __forceinline__ void act_both(float x, float& a, float& d)
     }
 }
 
-// 64 packed columns of this thread's row into a staging buffer and out.
-__device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage, uint32_t& sb, int lane,
-                                        const uint32_t (&lo)[16], const uint32_t (&hi)[16], int32_t x, int32_t y,
-                                        int32_t z)
+struct TileCtx {
+    int32_t row0;        // first row of this warp
+    int32_t col0;        // first column of this warp
+    int32_t tcol;        // the same, inside the accumulator
+    int32_t nchunks;     // 32-column chunks of this warp inside the matrix
+    int32_t batch;
+    int lane;
+    uint32_t stage;      // the warp's two staging buffers
+};
+
+// The staged box to global memory.
+__device__ __forceinline__ void send_box(const CUtensorMap* map, uint32_t buf, int lane, int32_t x, int32_t y,
+                                         int32_t z)
 {
-    const uint32_t buf = stage + sb * OUT_BUF_BYTES;
-    out_buffer_free(lane);
-    stage_half(buf, lane, 0, lo);
-    stage_half(buf, lane, 1, hi);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
         ptx::tma_store_3d(map, buf, x, y, z);
         ptx::bulk_commit_group();
     }
+}
+
+// 32 packed columns of this thread's row into a staging buffer and out.  A row
+// of the box is 64 bytes in the 64-byte swizzled layout: 16-byte chunk j of row
+// r sits at r * 64 + (j ^ (r / 2 % 4)) * 16, which keeps the eight lanes of a
+// store phase on different banks.  Rows and columns outside are not written.
+__device__ __forceinline__ void put_box(const CUtensorMap* map, const TileCtx& t, uint32_t& sb,
+                                        const uint32_t (&pk)[16], int32_t x)
+{
+    const uint32_t buf = t.stage + sb * OUT_BUF_BYTES;
+    out_buffer_free(t.lane);
+    const uint32_t at = buf + static_cast<uint32_t>(t.lane) * 64u;
+    const uint32_t sw = static_cast<uint32_t>(t.lane >> 1) & 3u;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+        ptx::st_shared_v4(at + ((j ^ sw) << 4), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+    send_box(map, buf, t.lane, x, t.row0, t.batch);
     sb ^= 1u;
 }
 
-// The same 32 rows x 64 columns transposed: row c of the box holds column c of
+// The same 32 rows x 32 columns transposed: row c of the box holds column c of
 // the tile, 32 values of 2 bytes.  Lane pairs swap halves so that each lane
 // writes one 32-bit word (two neighbouring rows of one column).
-__device__ __forceinline__ void put_box_t(const CUtensorMap* map, uint32_t stage, uint32_t& sb, int lane,
-                                          const uint32_t (&lo)[16], const uint32_t (&hi)[16], int32_t row,
-                                          int32_t col, int32_t z)
+__device__ __forceinline__ void put_box_t(const CUtensorMap* map, const TileCtx& t, uint32_t& sb,
+                                          const uint32_t (&pk)[16], int32_t x)
 {
-    const uint32_t buf = stage + sb * OUT_BUF_BYTES;
-    out_buffer_free(lane);
-    const bool odd = (lane & 1) != 0;
-    const uint32_t at = buf + static_cast<uint32_t>(odd ? 64 : 0) + static_cast<uint32_t>(lane >> 1) * 4u;
+    const uint32_t buf = t.stage + sb * OUT_BUF_BYTES;
+    out_buffer_free(t.lane);
+    const bool odd = (t.lane & 1) != 0;
+    const uint32_t at = buf + static_cast<uint32_t>(odd ? 64 : 0) + static_cast<uint32_t>(t.lane >> 1) * 4u;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t v = i < 16 ? lo[i & 15] : hi[i & 15];   // columns 2i, 2i + 1 of this row
-        const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
-        const uint32_t u = odd ? __byte_perm(o, v, 0x7632) : __byte_perm(v, o, 0x5410);
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, pk[i], 1);   // columns 2i, 2i + 1 of the other row
+        const uint32_t u = odd ? __byte_perm(o, pk[i], 0x7632) : __byte_perm(pk[i], o, 0x5410);
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 128u), "r"(u) : "memory");
     }
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        ptx::tma_store_3d(map, buf, row, col, z);
-        ptx::bulk_commit_group();
-    }
+    send_box(map, buf, t.lane, t.row0, x, t.batch);
     sb ^= 1u;
 }
 
-struct TileCtx {
-    int32_t row0;        // first row of this warp
-    int32_t col0;        // first column of the tile
-    int32_t nchunks;     // 32-column chunks inside the matrix
-    int32_t batch;
-    int lane;
-    uint32_t stage;      // the warp's staging buffers
-};
-
-// out = alpha D + beta C + diag I
+// out = alpha D + beta C + diag I (AUX: with the last two).
+template <bool AUX>
 __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
                                              bool mirror, uint32_t sb)
 {
@@ -476,98 +555,90 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
     const int32_t row = t.row0 + t.lane;
     const int32_t ncols = f.ncols;
     const __half* c_row = nullptr;
-    if (f.aux0 != nullptr && row < f.rows)
+    if (AUX && row < f.rows)
         c_row = static_cast<const __half*>(f.aux0) + t.batch * f.aux_batch + static_cast<int64_t>(row) * f.aux_ld;
     const CUtensorMap* map = &p.map[f.out[0]];
     const CUtensorMap* map_t = &p.map[f.out_t];
-    for (int c = 0; c < t.nchunks; c += 2) {
-        uint32_t pk[2][16];
+    // C's rows are 16-byte aligned and padded to 8 columns.  They may have been
+    // written earlier in this launch: read past L1, one chunk ahead.
+    uint4 cv[4];
+    auto load_c = [&](int c) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (c + h >= t.nchunks) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    pk[h][i] = 0u;   // columns past the output: clipped by the store
-                continue;
-            }
-            const int32_t x = t.col0 + (c + h) * 32;
-            // C's rows are 16-byte aligned and padded to 8 columns.  They may
-            // have been written earlier in this launch: read past L1.
-            uint4 cv[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cv[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (c_row != nullptr && x + 8 * j < ncols)
-                    cv[j] = __ldcg(reinterpret_cast<const uint4*>(c_row + x + 8 * j));
-            }
-            float v[32];
-            source32(src, c + h, v);
+        for (int j = 0; j < 4; ++j) {
+            const int32_t x = t.col0 + c * 32 + 8 * j;
+            cv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (c_row != nullptr && x < ncols)
+                cv[j] = __ldcg(reinterpret_cast<const uint4*>(c_row + x));
+        }
+    };
+    if (AUX)
+        load_c(0);
+#pragma unroll 1
+    for (int c = 0; c < t.nchunks; ++c) {
+        const int32_t x = t.col0 + c * 32;
+        uint32_t pk[16];
+        float v[32];
+        source32(src, t.tcol + c * 32, c, v);
+        if (AUX) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t cw[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&cw[q]));
-                    const int i = j * 8 + q * 2;
-                    v[i] = fmaf(alpha, v[i], beta * cf.x) + (x + i == row ? diag : 0.0f);
-                    v[i + 1] = fmaf(alpha, v[i + 1], beta * cf.y) + (x + i + 1 == row ? diag : 0.0f);
+                    v[j * 8 + q * 2] = fmaf(alpha, v[j * 8 + q * 2], beta * cf.x);
+                    v[j * 8 + q * 2 + 1] = fmaf(alpha, v[j * 8 + q * 2 + 1], beta * cf.y);
                 }
             }
+            if (c + 1 < t.nchunks)
+                load_c(c + 1);
+            if (x == t.row0) {   // this box is on the diagonal: column = lane
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pk[h][i] = pack_out(f16, v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < 32; ++i)
+                    v[i] += i == t.lane ? diag : 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] *= alpha;
         }
-        put_box(map, t.stage, sb, t.lane, pk[0], pk[1], t.col0 + c * 32, t.row0, t.batch);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack_out(f16, v[2 * i], v[2 * i + 1]);
+        put_box(map, t, sb, pk, x);
         if (mirror)
-            put_box_t(map_t, t.stage, sb, t.lane, pk[0], pk[1], t.row0, t.col0 + c * 32, t.batch);
+            put_box_t(map_t, t, sb, pk, x);
     }
     return sb;
 }
 
-// Gated tile: gate columns [0, 128) and linear columns [128, 256) of the
-// accumulator give 128 columns of G, U and H = act(G) U, H formed from the
-// fp32 sums and each rounded to bf16 once.
-template <int ACT>
+// Gated tile: TN / 2 gate columns and the same TN / 2 linear columns give G, U
+// and H = act(G) U, H formed from the fp32 sums and each rounded to bf16 once.
+template <int TN, int ACT>
 __device__ __forceinline__ uint32_t epi_glu_save(const Params& p, const Phase& f, const Source& src,
                                                  const TileCtx& t, uint32_t sb)
 {
-    for (int c = 0; c < t.nchunks; c += 2) {
-        uint32_t g[2][16], u[2][16], hh[2][16];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (c + h >= t.nchunks) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    g[h][i] = u[h][i] = hh[h][i] = 0u;
-                continue;
-            }
-            float a[32], b[32];
-            source32(src, c + h, a);
-            source32(src, BN_CTA / 32 + c + h, b);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                g[h][i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
-                u[h][i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
-                hh[h][i] = pack_bf16x2(act_apply(ACT, a[2 * i]) * b[2 * i], act_apply(ACT, a[2 * i + 1]) * b[2 * i + 1]);
-            }
-        }
+#pragma unroll 1
+    for (int c = 0; c < t.nchunks; ++c) {
         const int32_t x = t.col0 + c * 32;
-        put_box(&p.map[f.out[2]], t.stage, sb, t.lane, hh[0], hh[1], x, t.row0, 0);
-        put_box(&p.map[f.out[0]], t.stage, sb, t.lane, g[0], g[1], x, t.row0, 0);
-        put_box(&p.map[f.out[1]], t.stage, sb, t.lane, u[0], u[1], x, t.row0, 0);
+        float a[32], b[32];
+        source32(src, t.tcol + c * 32, c, a);
+        source32(src, TN / 2 + t.tcol + c * 32, TN / 128 + c, b);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack_bf16x2(act_apply(ACT, a[2 * i]) * b[2 * i], act_apply(ACT, a[2 * i + 1]) * b[2 * i + 1]);
+        put_box(&p.map[f.out[2]], t, sb, pk, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
+        put_box(&p.map[f.out[0]], t, sb, pk, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
+        put_box(&p.map[f.out[1]], t, sb, pk, x);
     }
     return sb;
-}
-
-// 32 columns (64 bytes) of this thread's row of a bf16 tensor; zeros outside.
-__device__ __forceinline__ void row32(const __nv_bfloat16* row, int32_t x, int32_t ncols, uint4 (&v)[4])
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (row != nullptr && x + 8 * j < ncols)
-            v[j] = __ldg(reinterpret_cast<const uint4*>(row + x + 8 * j));
-    }
 }
 
 // D = dH: dU = dH act(G), dG = dH U act'(G), and H = act(G) U again for dW2
@@ -584,76 +655,87 @@ __device__ __forceinline__ uint32_t epi_glu_grad(const Params& p, const Phase& f
         u_row = static_cast<const __nv_bfloat16*>(f.aux1) + static_cast<int64_t>(row) * f.aux_ld;
     }
     const int32_t ncols = f.ncols;
-    for (int c = 0; c < t.nchunks; c += 2) {
-        uint32_t dg[2][16], du[2][16], hh[2][16];
+    uint4 gv[4], uv[4];   // 32 columns of G and U, read one chunk ahead
+    auto load_gu = [&](int c) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (c + h >= t.nchunks) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    dg[h][i] = du[h][i] = hh[h][i] = 0u;
-                continue;
-            }
-            const int32_t x = t.col0 + (c + h) * 32;
-            uint4 gv[4], uv[4];
-            row32(g_row, x, ncols, gv);
-            row32(u_row, x, ncols, uv);
-            float d[32];
-            source32(src, c + h, d);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t gw[4] = {gv[j].x, gv[j].y, gv[j].z, gv[j].w};
-                const uint32_t uw[4] = {uv[j].x, uv[j].y, uv[j].z, uv[j].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int i = j * 4 + q;
-                    float a0, d0, a1, d1;
-                    act_both<ACT>(bf16_lo(gw[q]), a0, d0);
-                    act_both<ACT>(bf16_hi(gw[q]), a1, d1);
-                    const float u0 = bf16_lo(uw[q]), u1 = bf16_hi(uw[q]);
-                    dg[h][i] = pack_bf16x2(d[2 * i] * u0 * d0, d[2 * i + 1] * u1 * d1);
-                    du[h][i] = pack_bf16x2(d[2 * i] * a0, d[2 * i + 1] * a1);
-                    hh[h][i] = pack_bf16x2(a0 * u0, a1 * u1);
-                }
+        for (int j = 0; j < 4; ++j) {
+            const int32_t x = t.col0 + c * 32 + 8 * j;
+            gv[j] = uv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (g_row != nullptr && x < ncols) {
+                gv[j] = __ldg(reinterpret_cast<const uint4*>(g_row + x));
+                uv[j] = __ldg(reinterpret_cast<const uint4*>(u_row + x));
             }
         }
+    };
+    load_gu(0);
+#pragma unroll 1
+    for (int c = 0; c < t.nchunks; ++c) {
         const int32_t x = t.col0 + c * 32;
-        put_box(&p.map[f.out[0]], t.stage, sb, t.lane, dg[0], dg[1], x, t.row0, 0);
-        put_box(&p.map[f.out[1]], t.stage, sb, t.lane, du[0], du[1], x, t.row0, 0);
-        put_box(&p.map[f.out[2]], t.stage, sb, t.lane, hh[0], hh[1], x, t.row0, 0);
+        float d[32];
+        source32(src, t.tcol + c * 32, c, d);
+        uint32_t dg[16], du[16], hh[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t gw[4] = {gv[j].x, gv[j].y, gv[j].z, gv[j].w};
+            const uint32_t uw[4] = {uv[j].x, uv[j].y, uv[j].z, uv[j].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = j * 4 + q;
+                const float e0 = d[2 * i], e1 = d[2 * i + 1];
+                float a0, d0, a1, d1;
+                act_both<ACT>(bf16_lo(gw[q]), a0, d0);
+                act_both<ACT>(bf16_hi(gw[q]), a1, d1);
+                const float u0 = bf16_lo(uw[q]), u1 = bf16_hi(uw[q]);
+                dg[i] = pack_bf16x2(e0 * u0 * d0, e1 * u1 * d1);
+                du[i] = pack_bf16x2(e0 * a0, e1 * a1);
+                hh[i] = pack_bf16x2(a0 * u0, a1 * u1);
+            }
+        }
+        if (c + 1 < t.nchunks)
+            load_gu(c + 1);
+        put_box(&p.map[f.out[0]], t, sb, dg, x);
+        put_box(&p.map[f.out[1]], t, sb, du, x);
+        put_box(&p.map[f.out[2]], t, sb, hh, x);
     }
     return sb;
 }
 
-__device__ __noinline__ uint32_t epilogue_tile(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
+template <int TN>
+__device__ __forceinline__ uint32_t epilogue_tile(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
                                                bool mirror, uint32_t sb)
 {
-#define TFFN_EPI(FN)                                                                 \
-    switch (f.act) {                                                                 \
-    case TFFN_ACT_SILU: return FN<TFFN_ACT_SILU>(p, f, src, t, sb);                  \
-    case TFFN_ACT_GELU_TANH: return FN<TFFN_ACT_GELU_TANH>(p, f, src, t, sb);        \
-    case TFFN_ACT_RELU: return FN<TFFN_ACT_RELU>(p, f, src, t, sb);                  \
-    default: return FN<TFFN_ACT_NONE>(p, f, src, t, sb);                             \
-    }
     if (f.epi == EPI_GLU_SAVE) {
-        TFFN_EPI(epi_glu_save)
+        switch (f.act) {
+        case TFFN_ACT_SILU: return epi_glu_save<TN, TFFN_ACT_SILU>(p, f, src, t, sb);
+        case TFFN_ACT_GELU_TANH: return epi_glu_save<TN, TFFN_ACT_GELU_TANH>(p, f, src, t, sb);
+        case TFFN_ACT_RELU: return epi_glu_save<TN, TFFN_ACT_RELU>(p, f, src, t, sb);
+        default: return epi_glu_save<TN, TFFN_ACT_NONE>(p, f, src, t, sb);
+        }
     }
     if (f.epi == EPI_GLU_GRAD) {
-        TFFN_EPI(epi_glu_grad)
+        switch (f.act) {
+        case TFFN_ACT_SILU: return epi_glu_grad<TFFN_ACT_SILU>(p, f, src, t, sb);
+        case TFFN_ACT_GELU_TANH: return epi_glu_grad<TFFN_ACT_GELU_TANH>(p, f, src, t, sb);
+        case TFFN_ACT_RELU: return epi_glu_grad<TFFN_ACT_RELU>(p, f, src, t, sb);
+        default: return epi_glu_grad<TFFN_ACT_NONE>(p, f, src, t, sb);
+        }
     }
-#undef TFFN_EPI
-    return epi_poly(p, f, src, t, mirror, sb);
+    return f.aux0 != nullptr ? epi_poly<true>(p, f, src, t, mirror, sb) : epi_poly<false>(p, f, src, t, mirror, sb);
 }
 
-__device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank, int warp,
-                             int lane, uint32_t out_stage)
+template <int TN>
+__device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank,
+                             int warp, int lane, uint32_t out_stage)
 {
-    const uint32_t quad = static_cast<uint32_t>(warp & 3);   // TMEM lanes [32 quad, 32 quad + 32)
+    using G = Geo<TN>;
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);         // TMEM lanes [32 quad, 32 quad + 32)
+    const int32_t group = (warp - 2) / 4;                          // half of the tile's columns
+    const uint32_t part_warp = rank * EPI_WARPS + group * 4 + quad;
     uint32_t iter = 0, sb = 0;
     Ring ring;
     for (;;) {
         int4 task;
-        if (!engine::read_task(aux, w, ring, rank, true, lane, task) || task.x < 0)
+        if (!next_task(aux, w, ring, rank, true, lane, task) || task.x < 0)
             break;
         const Phase& f = p.ph[task.x];
         const uint32_t acc = iter & 1u;
@@ -661,65 +743,68 @@ __device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32
             break;
         ptx::tc_fence_after();
         TileCtx t;
-        const int32_t tile_cols = f.epi == EPI_GLU_SAVE ? BN_CTA : BN;
+        const int32_t cols = (f.epi == EPI_GLU_SAVE ? TN / 2 : TN) / 2;   // output columns of this warp
         t.row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA + static_cast<int32_t>(quad) * 32;
-        t.col0 = task.z * tile_cols;
+        t.tcol = group * cols;
+        t.col0 = task.z * 2 * cols + t.tcol;
         const int32_t left = f.ncols - t.col0;
-        t.nchunks = left >= tile_cols ? tile_cols / 32 : (left + 31) / 32;
+        t.nchunks = left >= cols ? cols / 32 : left > 0 ? (left + 31) / 32 : 0;
         t.batch = task_batch(task);
         t.lane = lane;
         t.stage = out_stage;
         Source src;
-        src.taddr = tmem_base + ((quad * 32u) << 16) + acc * BN;
+        src.taddr = tmem_base + ((quad * 32u) << 16) + acc * TN;
         src.parts = nullptr;
         src.nparts = 0;
-        const bool inside = t.row0 < f.rows;   // else nothing of this warp's rows is stored
+        src.part_vec = G::PART_VEC;
+        const bool inside = t.row0 < f.rows && t.nchunks > 0;   // else this warp stores nothing
         bool finish = inside;
         if (f.splits > 1) {
             // This part's sums to memory; the last part of the tile to arrive
             // (per warp) adds all of them, in part order.
             const int32_t tile = (t.batch * f.m_tiles + task.y - f.m_first) * f.n_tiles + task.z;
-            float4* part = reinterpret_cast<float4*>(f.partial) + static_cast<int64_t>(tile) * f.splits * PART_VEC +
-                           (rank * EPI_WARPS + quad) * PART_WARP_VEC + lane;
+            float4* part = reinterpret_cast<float4*>(f.partial) + static_cast<int64_t>(tile) * f.splits * G::PART_VEC +
+                           part_warp * G::PART_WARP_VEC + lane;
             if (inside) {
-                float4* dst = part + static_cast<int64_t>(task_part(task)) * PART_VEC;
-                const int chunks = f.epi == EPI_GLU_SAVE ? BN / 32 : t.nchunks;
-                for (int c = 0; c < chunks; ++c) {
-                    float v[32];
-                    source32(src, c, v);
+                float4* dst = part + static_cast<int64_t>(task_part(task)) * G::PART_VEC;
+                const int halves = f.epi == EPI_GLU_SAVE ? 2 : 1;   // gate and linear columns
+                for (int h = 0; h < halves; ++h)
+#pragma unroll 1
+                    for (int c = 0; c < t.nchunks; ++c) {
+                        float v[32];
+                        source32(src, h * (TN / 2) + t.tcol + c * 32, 0, v);
+                        float4* q = dst + (h * (TN / 128) + c) * 8 * 32;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __stcg(dst + (c * 8 + j) * 32, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-                }
+                        for (int j = 0; j < 8; ++j)
+                            __stcg(q + j * 32, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                    }
                 __threadfence();
                 __syncwarp();
                 uint32_t last = 0;
                 if (lane == 0) {
-                    uint32_t* ctr = p.counters + f.arrive_base + tile * TILE_PARTS + rank * EPI_WARPS + quad;
+                    uint32_t* ctr = p.counters + f.arrive_base + tile * TILE_PARTS + part_warp;
                     last = ptx::atom_add_acq_rel_gpu(ctr, 1u) == static_cast<uint32_t>(f.splits - 1) ? 1u : 0u;
+                    if (last)
+                        *ctr = 0u;   // every part has arrived: ready for the next phase that splits
                 }
                 finish = __shfl_sync(0xffffffffu, last, 0) != 0u;
                 __threadfence();
-            } else {
-                finish = false;
             }
             src.parts = part;
             src.nparts = f.splits;
-        }
-        const bool mirror = f.sym != 0 && task.y != task.z;
-        if (f.splits > 1) {
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                arrive_on_leader(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
+                arrive_read(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
         }
+        const bool mirror = f.sym != 0 && task.y != task.z * TN / BM;
         if (finish)
-            sb = epilogue_tile(p, f, src, t, mirror, sb);
+            sb = epilogue_tile<TN>(p, f, src, t, mirror, sb);
         if (f.splits <= 1) {
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                arrive_on_leader(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
+                arrive_read(ptx::smem_u32(&aux.tmem_empty[acc]), rank);
         }
         ++iter;
         // Count this warp's part of the tile once its stores are complete.  A
@@ -732,7 +817,7 @@ __device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32
                 uint32_t* ctr = p.counters + f.done_base + t.batch * f.done_stride;
                 ptx::red_relaxed_add_gpu(ctr + 1 + task.y, 1u);
                 if (mirror)
-                    ptx::red_relaxed_add_gpu(ctr + 1 + task.z, 1u);
+                    ptx::red_relaxed_add_gpu(ctr + 1 + task.z * TN / BM, 1u);
                 ptx::red_relaxed_add_gpu(ctr, 1u);
             }
             __syncwarp();
@@ -747,12 +832,14 @@ __device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32
 }
 
 // ------------------------------------------------------------------- kernel
+template <int TN>
 __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Aux& aux = *reinterpret_cast<Aux*>(stages + STAGES * STAGE_BYTES + OUT_BYTES);
+    constexpr int STAGES = Geo<TN>::STAGES, RING_BYTES = STAGES * Geo<TN>::STAGE_BYTES;
+    Aux<TN>& aux = *reinterpret_cast<Aux<TN>*>(stages + RING_BYTES + OUT_BYTES);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -787,16 +874,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
 
     if (warp == 0) {
         if (lane == 0)
-            run_a_loader(p, aux, stages, w, rank);
+            run_a_loader<TN>(p, aux, stages, w, rank);
     } else if (warp == B_LOADER_WARP) {
         if (lane == 0)
-            run_b_loader(p, aux, stages, w, rank);
+            run_b_loader<TN>(p, aux, stages, w, rank);
     } else if (warp == 1) {
         if (lane == 0 && rank == 0)
-            run_mma(p, aux, stages, w, tmem_base);
+            run_mma<TN>(p, aux, stages, w, tmem_base);
     } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
-        run_epilogue(p, aux, w, tmem_base, rank, warp, lane,
-                     ptx::smem_u32(stages + STAGES * STAGE_BYTES) +
+        run_epilogue<TN>(p, aux, w, tmem_base, rank, warp, lane,
+                     ptx::smem_u32(stages + RING_BYTES) +
                          static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES));
     }
     __syncwarp();

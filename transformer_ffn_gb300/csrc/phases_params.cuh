@@ -9,17 +9,15 @@ namespace phases {
 
 using engine::BK;
 using engine::BM;
-using engine::BN;
-using engine::BN_CTA;
-using engine::EPI_WARPS;
+
+constexpr int EPI_WARPS = 8;                           // per CTA
 
 constexpr int MAX_MAPS = 24;
 constexpr int MAX_PHASES = 24;
 constexpr int TILE_PARTS = 2 * EPI_WARPS;              // epilogue warps that finish one tile
-constexpr int PART_FLOATS = BM * BN;                   // fp32 partial sums of one split tile
 enum Epilogue : int32_t {
     EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16, read where it lies)
-    EPI_GLU_SAVE = 1,   // 128 columns of G and of U: out = {G, U, act(G) U}
+    EPI_GLU_SAVE = 1,   // half the columns G, half U: out = {G, U, act(G) U}
     EPI_GLU_GRAD = 2,   // D = dH: out = {dG, dU, H} from the saved G, U
 };
 
@@ -42,7 +40,7 @@ struct Phase {
     int32_t m_tiles, n_tiles;   // row tiles and column tiles of one batch entry
     int32_t batches;
     int32_t splits;             // K parts per tile
-    int32_t sym;                // lower triangle only (m_tiles == n_tiles), mirrored
+    int32_t sym;                // square result: row bands m_tiles, lower triangle only, mirrored
     int32_t group_m;            // row tiles per raster group
     int32_t nk[2];              // 64-deep k-blocks of the two K segments
     int8_t map_a[2], map_b[2];  // maps of the segments (GLU_SAVE: map_b = {W1, W3}, one segment)
@@ -73,6 +71,8 @@ struct Params {
     Phase ph[MAX_PHASES];
     int32_t n_phases;
     int32_t total;              // tickets
+    int32_t tile_cols;          // columns of a tile: 256 or 128
+    int32_t max_pairs;          // CTA pairs worth launching
     DevCtrl* ctrl;
     uint32_t* counters;         // zero when a launch starts, zeroed again by the last CTA out
     int32_t n_counters;

@@ -20,7 +20,7 @@ using phases::Dep;
 using phases::Phase;
 using PhaseParams = phases::Params;
 
-constexpr int64_t BM = phases::BM, BN = phases::BN, BK = phases::BK;
+constexpr int64_t BM = phases::BM, BK = phases::BK;
 constexpr int64_t MAX_DIM = int64_t(1) << 31;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -64,24 +64,30 @@ struct Maps {
         const cuuint32_t box[3] = {bx, by, 1};
         return add(3, m, dims, strides, box, sw);
     }
-    // An operand whose columns are the reduction index: 64 of them x 128 rows.
-    int k_major(const Mat& m) { return box3(m, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B); }
-    // An operand whose rows are the reduction index: 64 of them x 128 columns,
+    // An operand whose columns are the reduction index: 64 of them x `mn` rows
+    // (a CTA's share of the tile: 128 of A, half the tile's columns of B).
+    int k_major(const Mat& m, int64_t mn)
+    {
+        return box3(m, 64, static_cast<uint32_t>(mn), CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    // An operand whose rows are the reduction index: 64 of them x `mn` columns,
     // in one copy when the columns come in whole blocks of 64.
     static bool four(const Mat& m) { return m.cols % 64 == 0; }
-    int mn_major(const Mat& m)
+    int mn_major(const Mat& m, int64_t mn)
     {
         if (!four(m))
             return box3(m, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
         const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(m.rows), static_cast<cuuint64_t>(m.cols / 64),
                                     static_cast<cuuint64_t>(m.batch)};
         const cuuint64_t strides[3] = {static_cast<cuuint64_t>(m.ld) * 2, 128, batch_bytes(m)};
-        const cuuint32_t box[4] = {64, 64, 2, 1};
+        const cuuint32_t box[4] = {64, 64, static_cast<cuuint32_t>(mn / 64), 1};
         return add(4, m, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
-    int out(const Mat& m) { return box3(m, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B); }
-    int out_t(const Mat& m) { return box3(m, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE); }
+    int out(const Mat& m) { return box3(m, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B); }
+    int out_t(const Mat& m) { return box3(m, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE); }
 };
+
+constexpr int64_t A_ROWS = 128;   // A rows of a tile per CTA
 
 // A phase D [rows x ncols] = A B with K = nk0 (+ nk1) k-blocks.
 Phase make_phase(int64_t rows, int64_t ncols, int64_t tile_cols, int64_t k0, int64_t k1, int64_t raster_k)
@@ -104,18 +110,37 @@ Phase make_phase(int64_t rows, int64_t ncols, int64_t tile_cols, int64_t k0, int
     return f;
 }
 
-int64_t phase_tiles(const Phase& f)
+// Tiles of a phase, with tn columns each.
+int64_t phase_tiles(const Phase& f, int64_t tn)
 {
-    return (f.sym ? int64_t(f.m_tiles) * (f.m_tiles + 1) / 2 : int64_t(f.m_tiles) * f.n_tiles) * f.batches;
+    return (f.sym ? int64_t(f.m_tiles) * (f.m_tiles + 1) / 2 * (BM / tn) : int64_t(f.m_tiles) * f.n_tiles) * f.batches;
 }
 
-// K parts of a phase with fewer tiles than CTA pairs: as many as fill the
-// pairs, none shorter than eight k-blocks (a part's fp32 sums cost a write and
-// a read of the tile).
-int split_parts(int64_t tiles, int64_t nk, int64_t pairs)
+// Microseconds of a 64-deep k-block and of the rest of a task (hand-over,
+// first copies, epilogue), measured on GB300: what the choices of tile width
+// and K parts weigh against each other.
+double block_us(int64_t tn) { return tn == 256 ? 0.34 : 0.19; }
+double task_us(int64_t tn) { return tn == 256 ? 6.0 : 4.5; }
+
+// Time of `tiles` tiles of nk k-blocks, each in `parts` K parts, on `pairs`
+// CTA pairs: whole waves of tasks, and for split tiles the write and the
+// serial read of the parts' fp32 sums by the warp that adds them.
+double phase_us(int64_t tiles, int64_t nk, int64_t parts, int64_t pairs, int64_t tn)
 {
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(pairs / std::max<int64_t>(tiles, 1), nk / 8), 16);
-    return s < 2 ? 1 : static_cast<int>(s);
+    const double waves = static_cast<double>(div_up(tiles * parts, pairs));
+    const double join = parts > 1 ? 3.0 + 0.9 * static_cast<double>(parts) * static_cast<double>(tn) / 64 : 0.0;
+    return waves * static_cast<double>(div_up(nk, parts)) * block_us(tn) + task_us(tn) + join;
+}
+
+// K parts of a phase: as many as shorten it, none under eight k-blocks.  At
+// most one part's partial tile per CTA pair and tile width is kept.
+int split_parts(int64_t tiles, int64_t nk, int64_t pairs, int64_t tn)
+{
+    int best = 1;
+    for (int s = 2; s <= 16 && nk / s >= 8 && tiles * s <= 2 * pairs * 256 / tn; ++s)
+        if (phase_us(tiles, nk, s, pairs, tn) < phase_us(tiles, nk, best, pairs, tn))
+            best = s;
+    return best;
 }
 
 // The launch's table: tickets and counters are handed out in the order of add().
@@ -131,20 +156,29 @@ struct Table {
         f.done_stride = static_cast<int32_t>(1 + bands);
         counters += (1 + bands) * f.batches;
     }
+    // One split phase runs at a time, so all of a launch share the partial
+    // tiles and (the last part to arrive resets them) the arrival counters.
+    int64_t arrive_base = -1, arrivals = 0;
     void split(Phase& f, int parts, float* partial)
     {
         f.splits = parts;
         f.partial = partial;
-        f.arrive_base = static_cast<int32_t>(counters);
-        if (parts > 1)
-            counters += int64_t(f.m_tiles) * f.n_tiles * f.batches * phases::TILE_PARTS;
+        if (parts < 2)
+            return;
+        const int64_t words = int64_t(f.m_tiles) * f.n_tiles * f.batches * phases::TILE_PARTS;
+        if (words > arrivals) {
+            arrive_base = counters;
+            arrivals = words;
+            counters += words;
+        }
+        f.arrive_base = static_cast<int32_t>(arrive_base);
     }
     void add(const Phase& f)
     {
         Phase& q = p.ph[p.n_phases++];
         q = f;
         q.first = static_cast<int32_t>(tickets);
-        tickets += phase_tiles(f) * f.splits;
+        tickets += phase_tiles(f, p.tile_cols) * f.splits;
     }
 };
 
@@ -161,6 +195,10 @@ Dep depend(int mode, const Phase& by, int64_t tiles_band, int64_t all)
     return d;
 }
 
+// CTA pairs of a chain of dependent phases: no more than its largest phase has
+// tasks, so that later phases run on pairs that hold their code already.
+int32_t cap_pairs(int64_t tasks) { return static_cast<int32_t>(std::min<int64_t>(tasks, 1 << 20)); }
+
 int launch_table(PhaseParams& p, Table& t, const ApiSpace& ws, cudaStream_t s)
 {
     if (t.tickets >= MAX_DIM || t.counters > static_cast<int64_t>(ws.counter_words))
@@ -174,8 +212,8 @@ int launch_table(PhaseParams& p, Table& t, const ApiSpace& ws, cudaStream_t s)
 }
 
 // ------------------------------------------------------------- gated FFN
-// Bytes of fp32 partial tiles: at most one tile per CTA pair and phase.
-size_t partial_bytes(int sms) { return size_t(sms / 2 + 1) * phases::PART_FLOATS * 4; }
+// Bytes of fp32 partial tiles (split_parts keeps to two 256-column tiles per CTA pair).
+size_t partial_bytes(int sms) { return size_t(sms / 2 + 1) * 2 * BM * 256 * 4; }
 
 struct GluSpace {
     size_t dg, du, h, part, total;   // offsets into the workspace's data
@@ -252,12 +290,20 @@ int glu_train_forward(const void* X, const void* W1, const void* W3, const void*
     const Mat x = dense(X, M, N), w1 = dense(W1, N, O), w3 = dense(W3, N, O), w2 = dense(W2, O, P);
     const Mat h = dense(ws.data + gs.h, M, O);
 
-    Phase up = make_phase(M, O, phases::BN_CTA, N, 0, N);
+    // the tile width that is expected to be faster: a gated tile makes half its columns of H
+    auto cost = [&](int64_t tn) {
+        const int64_t tiles = bands * div_up(P, tn), nk = div_up(O, BK);
+        return phase_us(bands * div_up(O, tn / 2), div_up(N, BK), 1, pairs, tn) +
+               phase_us(tiles, nk, split_parts(tiles, nk, pairs, tn), pairs, tn);
+    };
+    const int64_t tn = cost(128) < cost(256) ? 128 : 256;
+    p.tile_cols = static_cast<int32_t>(tn);
+    Phase up = make_phase(M, O, tn / 2, N, 0, N);
     up.epi = phases::EPI_GLU_SAVE;
     up.act = act;
-    up.map_a[0] = static_cast<int8_t>(mp.k_major(x));
-    up.map_b[0] = static_cast<int8_t>(mp.mn_major(w1));
-    up.map_b[1] = static_cast<int8_t>(mp.mn_major(w3));
+    up.map_a[0] = static_cast<int8_t>(mp.k_major(x, A_ROWS));
+    up.map_b[0] = static_cast<int8_t>(mp.mn_major(w1, tn / 2));
+    up.map_b[1] = static_cast<int8_t>(mp.mn_major(w3, tn / 2));
     up.b_mn = 1;
     up.b4 = Maps::four(w1);
     up.out[0] = static_cast<int8_t>(mp.out(dense(G, M, O)));
@@ -265,16 +311,17 @@ int glu_train_forward(const void* X, const void* W1, const void* W3, const void*
     up.out[2] = static_cast<int8_t>(mp.out(h));
     t.count_done(up, bands);
 
-    Phase down = make_phase(M, P, BN, O, 0, N);
-    down.map_a[0] = static_cast<int8_t>(mp.k_major(h));
-    down.map_b[0] = static_cast<int8_t>(mp.mn_major(w2));
+    Phase down = make_phase(M, P, tn, O, 0, N);
+    down.map_a[0] = static_cast<int8_t>(mp.k_major(h, A_ROWS));
+    down.map_b[0] = static_cast<int8_t>(mp.mn_major(w2, tn / 2));
     down.b_mn = 1;
     down.b4 = Maps::four(w2);
     down.out[0] = static_cast<int8_t>(mp.out(dense(Y, M, P)));
-    down.dep_a = depend(phases::DEP_BAND, up, up.n_tiles, phase_tiles(up));
+    down.dep_a = depend(phases::DEP_BAND, up, up.n_tiles, phase_tiles(up, tn));
     if (mp.failed)
         return TFFN_ERR_INVALID_ARG;
-    const int parts = split_parts(phase_tiles(down), down.nk[0], pairs);
+    const int parts = split_parts(phase_tiles(down, tn), down.nk[0], pairs, tn);
+    p.max_pairs = cap_pairs(std::max(phase_tiles(up, tn), phase_tiles(down, tn) * parts));
     t.split(down, parts, reinterpret_cast<float*>(ws.data + gs.part));
     add_interleaved(t, up, down, bands, parts > 1 ? bands : band_group(bands, up.group_m, MAX_GROUPS));
     api_timing_start(s);
@@ -314,12 +361,21 @@ int glu_backward(const void* dY, const void* X, const void* W1, const void* W3, 
               w2 = dense(W2, O, P);
     const Mat dg = dense(ws.data + gs.dg, M, O), du = dense(ws.data + gs.du, M, O), h = dense(ws.data + gs.h, M, O);
 
+    auto cost = [&](int64_t tn) {
+        const int64_t tiles = bands * div_up(N, tn), nk = 2 * div_up(O, BK);
+        const int64_t weights = 2 * div_up(N, BM) * div_up(O, tn) + div_up(O, BM) * div_up(P, tn);
+        return phase_us(bands * div_up(O, tn), div_up(P, BK), 1, pairs, tn) +
+               phase_us(tiles, nk, split_parts(tiles, nk, pairs, tn), pairs, tn) +
+               phase_us(weights, div_up(M, BK), 1, pairs, tn);
+    };
+    const int64_t tn = cost(128) < cost(256) ? 128 : 256;
+    p.tile_cols = static_cast<int32_t>(tn);
     // dH = dY W2^T, and from it dG, dU and H
-    Phase up = make_phase(M, O, BN, P, 0, P);
+    Phase up = make_phase(M, O, tn, P, 0, P);
     up.epi = phases::EPI_GLU_GRAD;
     up.act = act;
-    up.map_a[0] = static_cast<int8_t>(mp.k_major(dy));
-    up.map_b[0] = static_cast<int8_t>(mp.k_major(w2));
+    up.map_a[0] = static_cast<int8_t>(mp.k_major(dy, A_ROWS));
+    up.map_b[0] = static_cast<int8_t>(mp.k_major(w2, tn / 2));
     up.out[0] = static_cast<int8_t>(mp.out(dg));
     up.out[1] = static_cast<int8_t>(mp.out(du));
     up.out[2] = static_cast<int8_t>(mp.out(h));
@@ -327,25 +383,25 @@ int glu_backward(const void* dY, const void* X, const void* W1, const void* W3, 
     up.aux1 = U;
     up.aux_ld = O;
     t.count_done(up, bands);
-    const int64_t up_tiles = phase_tiles(up);
+    const int64_t up_tiles = phase_tiles(up, tn);
 
     // dX = dG W1^T + dU W3^T, one accumulation over both
-    Phase down = make_phase(M, N, BN, O, O, P);
-    down.map_a[0] = static_cast<int8_t>(mp.k_major(dg));
-    down.map_a[1] = static_cast<int8_t>(mp.k_major(du));
-    down.map_b[0] = static_cast<int8_t>(mp.k_major(w1));
-    down.map_b[1] = static_cast<int8_t>(mp.k_major(w3));
+    Phase down = make_phase(M, N, tn, O, O, P);
+    down.map_a[0] = static_cast<int8_t>(mp.k_major(dg, A_ROWS));
+    down.map_a[1] = static_cast<int8_t>(mp.k_major(du, A_ROWS));
+    down.map_b[0] = static_cast<int8_t>(mp.k_major(w1, tn / 2));
+    down.map_b[1] = static_cast<int8_t>(mp.k_major(w3, tn / 2));
     down.out[0] = static_cast<int8_t>(mp.out(dense(dX, M, N)));
     down.dep_a = depend(phases::DEP_BAND, up, up.n_tiles, up_tiles);
 
     // dW = A^T B over the rows of A and B
     auto weight = [&](const Mat& a, const Mat& b, void* out, bool a_made, bool b_made) {
-        Phase f = make_phase(a.cols, b.cols, BN, M, 0, M);
+        Phase f = make_phase(a.cols, b.cols, tn, M, 0, M);
         f.a_mn = f.b_mn = 1;
         f.a4 = Maps::four(a);
         f.b4 = Maps::four(b);
-        f.map_a[0] = static_cast<int8_t>(mp.mn_major(a));
-        f.map_b[0] = static_cast<int8_t>(mp.mn_major(b));
+        f.map_a[0] = static_cast<int8_t>(mp.mn_major(a, A_ROWS));
+        f.map_b[0] = static_cast<int8_t>(mp.mn_major(b, tn / 2));
         f.out[0] = static_cast<int8_t>(mp.out(dense(out, a.cols, b.cols)));
         if (a_made)
             f.dep_a = depend(phases::DEP_ALL, up, up.n_tiles, up_tiles);
@@ -358,7 +414,9 @@ int glu_backward(const void* dY, const void* X, const void* W1, const void* W3, 
     const Phase f3 = weight(x, du, dW3, false, true);
     if (mp.failed)
         return TFFN_ERR_INVALID_ARG;
-    const int parts = split_parts(phase_tiles(down), down.nk[0] + down.nk[1], pairs);
+    const int parts = split_parts(phase_tiles(down, tn), down.nk[0] + down.nk[1], pairs, tn);
+    p.max_pairs = cap_pairs(std::max(up_tiles, phase_tiles(down, tn) * parts + phase_tiles(f2, tn) +
+                                                   phase_tiles(f1, tn) + phase_tiles(f3, tn)));
     t.split(down, parts, reinterpret_cast<float*>(ws.data + gs.part));
     add_interleaved(t, up, down, bands, parts > 1 ? bands : band_group(bands, up.group_m, MAX_GROUPS));
     t.add(f2);
@@ -437,27 +495,44 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
     }
     const Mat A{ws.data + q.a, side, side, q.lds, count, side * q.lds, true};
     const Mat B{ws.data + q.b, side, side, q.lds, count, side * q.lds, true};
-    const int xk[2] = {mp.k_major(x[0]), mp.k_major(x[1])};
-    const int xm[2] = {mp.mn_major(x[0]), mp.mn_major(x[1])};
-    const int xo[2] = {mp.out(x[0]), mp.out(x[1])};
-    const int ak = mp.k_major(A), ao = mp.out(A), at = mp.out_t(A);
-    const int bk = mp.k_major(B), bo = mp.out(B), bt = mp.out_t(B);
+    const int64_t sb = div_up(side, BM);
+    const int64_t gram_k = tall ? m : n;
+    auto cost = [&](int64_t tn) {
+        const int64_t tri = sb * (sb + 1) / 2 * (BM / tn) * count, nk = div_up(gram_k, BK);
+        return phase_us(tri, nk, split_parts(tri, nk, pairs, tn), pairs, tn) +
+               phase_us(tri, div_up(side, BK), 1, pairs, tn) +
+               phase_us(div_up(m, BM) * div_up(q.ldx, tn) * count, div_up(side, BK), 1, pairs, tn);
+    };
+    const int64_t tn = cost(128) < cost(256) ? 128 : 256;
+    p.tile_cols = static_cast<int32_t>(tn);
+    // X as A and as B operand: K-major in one product, MN-major in the other
+    int xa[2], xb[2], xc[2], xo[2];   // gram's A and B operands, the update's X operand, output
+    for (int i = 0; i < 2; ++i) {
+        xa[i] = tall ? mp.mn_major(x[i], A_ROWS) : mp.k_major(x[i], A_ROWS);
+        xb[i] = tall ? mp.mn_major(x[i], tn / 2) : mp.k_major(x[i], tn / 2);
+        xc[i] = tall ? mp.k_major(x[i], A_ROWS) : mp.mn_major(x[i], tn / 2);
+        xo[i] = mp.out(x[i]);
+    }
+    const int aa = mp.k_major(A, A_ROWS), ab = mp.k_major(A, tn / 2), ao = mp.out(A), at = mp.out_t(A);
+    const int bk = mp.k_major(B, tall ? tn / 2 : A_ROWS), bo = mp.out(B), bt = mp.out_t(B);
     const int oo = last ? mp.out(out) : 0;
     if (mp.failed)
         return TFFN_ERR_INVALID_ARG;
     float* partial = reinterpret_cast<float*>(ws.data + q.part);
-    const int64_t sb = div_up(side, BM);
+    int64_t most = 1;   // tasks of the largest phase
 
     Phase prev;   // the update that made the current X
     bool has_prev = false;
     for (int i = 0; i < steps; ++i) {
         // A = X X^T (tall: X^T X) / 64^2
-        Phase gram = make_phase(side, side, BN, tall ? m : n, 0, tall ? m : n);
+        Phase gram = make_phase(side, side, tn, gram_k, 0, gram_k);
         gram.batches = static_cast<int32_t>(count);
         gram.sym = 1;
+        gram.n_tiles = static_cast<int32_t>(sb * (BM / tn));
         gram.f16 = gram.out_f16 = 1;
         gram.a_mn = gram.b_mn = gram.a4 = gram.b4 = tall ? 1 : 0;
-        gram.map_a[0] = gram.map_b[0] = static_cast<int8_t>(tall ? xm[cur] : xk[cur]);
+        gram.map_a[0] = static_cast<int8_t>(xa[cur]);
+        gram.map_b[0] = static_cast<int8_t>(xb[cur]);
         gram.alpha = 1.0f / (NS_SCALE * NS_SCALE);
         gram.out[0] = static_cast<int8_t>(ao);
         gram.out_t = static_cast<int8_t>(at);
@@ -466,15 +541,18 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
                                              int64_t(prev.m_tiles) * prev.n_tiles);
         }
         t.count_done(gram, sb);
-        t.split(gram, split_parts(phase_tiles(gram), gram.nk[0], pairs), partial);
+        t.split(gram, split_parts(phase_tiles(gram, tn), gram.nk[0], pairs, tn), partial);
+        most = std::max(most, phase_tiles(gram, tn) * gram.splits);
         t.add(gram);
 
         // B = a I + b A + c A A
-        Phase sq = make_phase(side, side, BN, side, 0, side);
+        Phase sq = make_phase(side, side, tn, side, 0, side);
         sq.batches = static_cast<int32_t>(count);
         sq.sym = 1;
+        sq.n_tiles = gram.n_tiles;
         sq.f16 = sq.out_f16 = 1;
-        sq.map_a[0] = sq.map_b[0] = static_cast<int8_t>(ak);
+        sq.map_a[0] = static_cast<int8_t>(aa);
+        sq.map_b[0] = static_cast<int8_t>(ab);
         sq.alpha = NS_C;
         sq.beta = NS_B;
         sq.diag = NS_A;
@@ -483,33 +561,33 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
         sq.aux_batch = A.bs;
         sq.out[0] = static_cast<int8_t>(bo);
         sq.out_t = static_cast<int8_t>(bt);
-        sq.dep_a = sq.dep_b = depend(phases::DEP_BAND, gram, sb, sb * (sb + 1) / 2);
+        sq.dep_a = sq.dep_b = depend(phases::DEP_BAND, gram, gram.n_tiles, phase_tiles(gram, tn) / count);
         t.count_done(sq, sb);
         t.split(sq, 1, partial);
         t.add(sq);
 
         // X <- B X (tall: X B)
         const bool end = last && i + 1 == steps;
-        Phase up = make_phase(m, end ? n : q.ldx, BN, side, 0, side);
+        Phase up = make_phase(m, end ? n : q.ldx, tn, side, 0, side);
         up.batches = static_cast<int32_t>(count);
         up.f16 = 1;
         up.out_f16 = end ? 0 : 1;
         up.alpha = end ? 1.0f / NS_SCALE : 1.0f;
         up.out[0] = static_cast<int8_t>(end ? oo : xo[cur ^ 1]);
-        const Dep on_b = depend(phases::DEP_BAND, sq, sb, sb * (sb + 1) / 2);
+        const Dep on_b = depend(phases::DEP_BAND, sq, sq.n_tiles, phase_tiles(sq, tn) / count);
         Dep on_x;
         std::memset(&on_x, 0, sizeof(on_x));
         if (has_prev)
             on_x = depend(tall ? phases::DEP_BAND : phases::DEP_ALL, prev, prev.n_tiles,
                           int64_t(prev.m_tiles) * prev.n_tiles);
         if (tall) {
-            up.map_a[0] = static_cast<int8_t>(xk[cur]);
+            up.map_a[0] = static_cast<int8_t>(xc[cur]);
             up.map_b[0] = static_cast<int8_t>(bk);
             up.dep_a = on_x;
             up.dep_b = on_b;
         } else {
             up.map_a[0] = static_cast<int8_t>(bk);
-            up.map_b[0] = static_cast<int8_t>(xm[cur]);
+            up.map_b[0] = static_cast<int8_t>(xc[cur]);
             up.b_mn = up.b4 = 1;
             up.dep_a = on_b;
             up.dep_b = on_x;
@@ -517,10 +595,12 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
         t.count_done(up, up.m_tiles);
         t.split(up, 1, partial);
         t.add(up);
+        most = std::max(most, phase_tiles(up, tn));
         prev = up;
         has_prev = true;
         cur ^= 1;
     }
+    p.max_pairs = cap_pairs(most);
     return launch_table(p, t, ws, s);
 }
 
