@@ -19,8 +19,8 @@
 // smaller tickets, so the launch finishes with any number of resident CTAs.
 //
 // The main loop is the FFN engine's (engine.cuh): clusters of two CTAs, a ring
-// of 192 KiB of stages per CTA, an A loader that claims tickets one task ahead,
-// a B loader, one MMA thread.  The epilogue has eight warps, two per tensor
+// of 192 KiB of stages per CTA, an A and a B loader and one MMA thread; a
+// scheduler thread claims the tickets.  The epilogue has eight warps, two per tensor
 // memory lane quadrant and so two per scheduler, each taking half of the
 // tile's columns, 32 at a time, through two 2 KiB staging buffers: a tile's
 // epilogue is bound by instructions and latency, not by memory, and its time is
@@ -46,8 +46,10 @@ using engine::TMEM_COLS;
 using engine::wait_own;
 
 constexpr int B_LOADER_WARP = 2 + EPI_WARPS;
-constexpr int NUM_THREADS = 32 * (3 + EPI_WARPS);
-constexpr uint32_t TASK_CONSUMERS = 1 + 1 + EPI_WARPS + 1 + 1 + EPI_WARPS;   // as engine::TASK_CONSUMERS
+constexpr int SCHEDULER_WARP = 3 + EPI_WARPS;
+constexpr int NUM_THREADS = 32 * (4 + EPI_WARPS);
+// Arrivals that free a task slot: both CTAs' loaders and epilogue warps, the MMA thread.
+constexpr uint32_t TASK_CONSUMERS = 2 * (2 + EPI_WARPS) + 1;
 constexpr int OUT_BUF_BYTES = 32 * 32 * 2;                 // 32 rows x 32 columns
 constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;   // 32 KiB
 
@@ -69,6 +71,7 @@ struct Aux {
     uint64_t tmem_empty[2];
     uint64_t task_full[TASK_SLOTS];
     uint64_t task_empty[TASK_SLOTS];
+    uint64_t taken;                 // leader: the A loader has read the last task
     uint64_t drain;
     int4 task[TASK_SLOTS];
     uint32_t tmem_base;
@@ -223,10 +226,30 @@ __device__ __forceinline__ bool next_task(AuxT& aux, const WaitCtx& w, Ring& r, 
 }
 
 // ----------------------------------------------------------------- loaders
-// A loader of one CTA; the leader's also claims the tickets (the next task is
-// published one task ahead, so its hand-over never waits for the claim).  A
-// pair holds two tickets beyond the one it runs, all larger, so the smallest
+// Scheduler (leader): claims tickets and hands each task to both CTAs' rings,
+// the next one as soon as the A loader has taken the last, so that a short
+// task's copies wait neither for a claim's round trip nor for its decoding.  A
+// pair holds two tickets beyond the one it loads, all larger, so the smallest
 // unfinished ticket is always some pair's current task.
+template <int TN>
+__device__ void run_scheduler(const Params& p, Aux<TN>& aux, const WaitCtx& w)
+{
+    Ring ring;
+    uint32_t ticket = atomicAdd(&p.ctrl->ticket, 1u);
+    for (uint32_t n = 0;; ++n) {
+        const int4 task = decode_ticket<TN>(p, static_cast<int32_t>(ticket));
+        if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_empty[ring.slot]), ring.phase ^ 1u, SITE_TASK_EMPTY))
+            return;
+        engine::publish_task(aux, ring, task);
+        if (task.x < 0)
+            return;
+        ticket = atomicAdd(&p.ctrl->ticket, 1u);
+        if (!wait_mbar(w, ptx::smem_u32(&aux.taken), n & 1u, SITE_TASK_EMPTY))
+            return;
+    }
+}
+
+// A loader of one CTA.
 template <int TN>
 __device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
 {
@@ -237,31 +260,12 @@ __device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, con
     int32_t last_phase[STAGES];
     for (int s = 0; s < STAGES; ++s)
         last_phase[s] = -1;
-    // The ticket after the published one is already requested: its atomic's
-    // round trip passes behind a task's copies.
-    uint32_t ticket = rank == 0 ? atomicAdd(&p.ctrl->ticket, 1u) : 0u;
-    auto claim_publish = [&](int4& out) -> bool {
-        out = decode_ticket<TN>(p, static_cast<int32_t>(ticket));
-        if (out.x >= 0)
-            ticket = atomicAdd(&p.ctrl->ticket, 1u);
-        if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_empty[ring.slot]), ring.phase ^ 1u, SITE_TASK_EMPTY))
-            return false;
-        engine::publish_task(aux, ring, out);
-        return true;
-    };
-    int4 ahead = make_int4(-1, 0, 0, 0);
-    const bool started = rank != 0 || claim_publish(ahead);
-    while (started) {
+    for (;;) {
         int4 task;
-        if (rank == 0) {
-            task = ahead;
-            if (task.x >= 0 && !claim_publish(ahead))
-                break;
-        } else if (!next_task(aux, w, ring, rank, false, 0, task)) {
+        if (!next_task(aux, w, ring, rank, false, 0, task) || task.x < 0)
             break;
-        }
-        if (task.x < 0)
-            break;
+        if (rank == 0)
+            ptx::mbar_arrive(ptx::smem_u32(&aux.taken));
         const Phase& f = p.ph[task.x];
         const int32_t batch = task_batch(task);
         const int32_t row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA;
@@ -284,7 +288,7 @@ __device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, con
                 ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
             const bool second = kb >= nk0;
             load_operand<BM_CTA>(ptx::smem_u32(stages + stage * STAGE_BYTES), second ? map1 : map0, fb,
-                         (second ? kb - nk0 : kb) * BK, row0, batch, mn, four);
+                                 (second ? kb - nk0 : kb) * BK, row0, batch, mn, four);
             last_phase[stage] = static_cast<int32_t>(phase);
             if (++stage == STAGES) {
                 stage = 0;
@@ -408,6 +412,11 @@ struct Source {
     int part_vec;            // float4 from one part to the next
 };
 
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b)
+{
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // 32 columns: the accumulator's from column `col`, or the parts' chunk `c`.
 __device__ __forceinline__ void source32(const Source& s, int col, int c, float (&v)[32])
 {
@@ -421,31 +430,40 @@ __device__ __forceinline__ void source32(const Source& s, int col, int c, float 
             v[i] = __uint_as_float(r[i]);
         return;
     }
-    const float4* src = s.parts + c * 8 * 32;
-    float4 x[8];
+    // 16 columns at a time, four parts' loads in flight: each round costs one
+    // trip to L2
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        x[j] = __ldcg(src + j * 32);
-    for (int q = 1; q < s.nparts; ++q) {
-        src += s.part_vec;
-        float4 y[8];
+    for (int h = 0; h < 2; ++h) {
+        const float4* src = s.parts + (c * 8 + h * 4) * 32;
+        float4 x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = __ldcg(src + j * 32);
+        for (int j = 0; j < 4; ++j)
+            x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int q = 0;
+        for (; q + 4 <= s.nparts; q += 4, src += 4 * s.part_vec) {
+            float4 y[4][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j].x += y[j].x;
-            x[j].y += y[j].y;
-            x[j].z += y[j].z;
-            x[j].w += y[j].w;
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[k][j] = __ldcg(src + k * s.part_vec + j * 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = add4(x[j], y[k][j]);
         }
-    }
+        for (; q < s.nparts; ++q, src += s.part_vec)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        v[4 * j] = x[j].x;
-        v[4 * j + 1] = x[j].y;
-        v[4 * j + 2] = x[j].z;
-        v[4 * j + 3] = x[j].w;
+            for (int j = 0; j < 4; ++j)
+                x[j] = add4(x[j], __ldcg(src + j * 32));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[h * 16 + 4 * j] = x[j].x;
+            v[h * 16 + 4 * j + 1] = x[j].y;
+            v[h * 16 + 4 * j + 2] = x[j].z;
+            v[h * 16 + 4 * j + 3] = x[j].w;
+        }
     }
 }
 
@@ -858,6 +876,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
             ptx::mbar_init(ptx::smem_u32(&aux.task_empty[s]), TASK_CONSUMERS);
         }
         ptx::mbar_init(ptx::smem_u32(&aux.drain), 1);
+        ptx::mbar_init(ptx::smem_u32(&aux.taken), 1);
         aux.abort = 0u;
         ptx::fence_barrier_init();
     }
@@ -881,7 +900,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
     } else if (warp == 1) {
         if (lane == 0 && rank == 0)
             run_mma<TN>(p, aux, stages, w, tmem_base);
-    } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
+    } else if (warp == SCHEDULER_WARP) {
+        if (lane == 0 && rank == 0)
+            run_scheduler<TN>(p, aux, w);
+    } else {
         run_epilogue<TN>(p, aux, w, tmem_base, rank, warp, lane,
                      ptx::smem_u32(stages + RING_BYTES) +
                          static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES));

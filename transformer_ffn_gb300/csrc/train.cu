@@ -118,17 +118,20 @@ int64_t phase_tiles(const Phase& f, int64_t tn)
 
 // Microseconds of a 64-deep k-block and of the rest of a task (hand-over,
 // first copies, epilogue), measured on GB300: what the choices of tile width
-// and K parts weigh against each other.
-double block_us(int64_t tn) { return tn == 256 ? 0.34 : 0.19; }
-double task_us(int64_t tn) { return tn == 256 ? 6.0 : 4.5; }
+// and K parts weigh against each other.  A 128-column tile's k-block is hardly
+// shorter than a 256-column tile's, so it pays only where the latter would
+// leave most CTA pairs idle.
+double block_us(int64_t tn) { return tn == 256 ? 0.34 : 0.30; }
+double task_us(int64_t tn) { return tn == 256 ? 8.0 : 6.0; }
 
 // Time of `tiles` tiles of nk k-blocks, each in `parts` K parts, on `pairs`
-// CTA pairs: whole waves of tasks, and for split tiles the write and the
-// serial read of the parts' fp32 sums by the warp that adds them.
+// CTA pairs: whole waves of tasks, and for split tiles the write and the read
+// (four parts a round) of the parts' fp32 sums.
 double phase_us(int64_t tiles, int64_t nk, int64_t parts, int64_t pairs, int64_t tn)
 {
     const double waves = static_cast<double>(div_up(tiles * parts, pairs));
-    const double join = parts > 1 ? 3.0 + 0.9 * static_cast<double>(parts) * static_cast<double>(tn) / 64 : 0.0;
+    const double join = parts > 1 ? 5.0 + 3.0 * static_cast<double>(div_up(parts, 4)) * static_cast<double>(tn) / 256
+                                  : 0.0;
     return waves * static_cast<double>(div_up(nk, parts)) * block_us(tn) + task_us(tn) + join;
 }
 
