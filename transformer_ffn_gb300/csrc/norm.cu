@@ -38,26 +38,13 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
     return __float2bfloat16_rn(v);
 }
 
-// Words of 16, 8, 4 or 2 bytes.
+// Words of 16 or 4 bytes.
 template <int B>
 struct Word;
 template <>
 struct Word<16> { using type = uint4; };
 template <>
-struct Word<8> { using type = uint2; };
-template <>
 struct Word<4> { using type = uint32_t; };
-template <>
-struct Word<2> { using type = uint16_t; };
-
-// Streaming load and store: the tensors are read and written once.
-template <typename T, int VW>
-__device__ __forceinline__ Vec<T, VW> load_stream(const T* p)
-{
-    using W = typename Word<sizeof(T) * VW>::type;
-    const W w = __ldcs(reinterpret_cast<const W*>(p));
-    return *reinterpret_cast<const Vec<T, VW>*>(&w);
-}
 
 template <typename T, int VW>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, VW>& v)
@@ -66,9 +53,11 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, VW>& v)
     *reinterpret_cast<W*>(p) = *reinterpret_cast<const W*>(&v);
 }
 
-// VW parameters from column c; `absent` where there is no tensor.
+// VW parameters from column c (columns outside [0, N) do not matter); `absent`
+// where there is no tensor.
 template <int VW>
-__device__ __forceinline__ void load_param(const void* p, bool f32, int64_t c, float absent, bool vec, float (&v)[VW])
+__device__ __forceinline__ void load_param(const void* p, bool f32, int64_t c, int64_t N, float absent, bool vec,
+                                           float (&v)[VW])
 {
     if (p == nullptr) {
 #pragma unroll
@@ -88,7 +77,7 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, int64_t c, f
         } else {
 #pragma unroll
             for (int j = 0; j < VW; ++j)
-                v[j] = __ldg(q + j);
+                v[j] = c + j >= 0 && c + j < N ? __ldg(q + j) : 0.0f;
         }
     } else {
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + c;
@@ -104,7 +93,7 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, int64_t c, f
         } else {
 #pragma unroll
             for (int j = 0; j < VW; ++j)
-                v[j] = __bfloat162float(q[j]);
+                v[j] = c + j >= 0 && c + j < N ? __bfloat162float(q[j]) : 0.0f;
         }
     }
 }
@@ -144,90 +133,267 @@ struct FwdArgs {
     int p32, pvec;
 };
 
-// A row's columns stay in the registers of its TPR threads (NV vectors of VW
-// each), so the row is read once and the variance is the exact second pass
-// over (S - mu).  Rows of up to 512 bytes a thread's warp owns; longer rows
-// take a block.
-template <typename T, int VW, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const FwdArgs a)
+// Elements of a row in front of its first whole vector's columns: bf16 rows of
+// odd length start between two 4-byte words every other time, and are then
+// taken word by word from one element earlier (VW = 2).  0 or 1.
+template <typename T, int VW>
+__device__ __forceinline__ int row_shift(const T* base, int64_t row, int64_t N)
 {
-    __shared__ float red[2][TPR <= 32 ? 1 : TPR / 32];
-    constexpr int ROWS = TPR < 128 ? 128 / TPR : 1;   // rows per block
-    const int t = threadIdx.x % TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR;
-    if (row >= a.T)
-        return;   // whole warps: a block with several warps per row holds one row
-    const T* x = static_cast<const T*>(a.X) + row * a.N;
-    const T* r = a.R == nullptr ? nullptr : static_cast<const T*>(a.R) + row * a.N;
-    Vec<T, VW> xv[NV], rv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-        if (c < a.N) {
-            xv[i] = load_stream<T, VW>(x + c);
-            if (r != nullptr)
-                rv[i] = load_stream<T, VW>(r + c);
+    return VW == 2 ? static_cast<int>(((reinterpret_cast<uintptr_t>(base) / sizeof(T)) + row * N) & 1) : 0;
+}
+
+// A word may hold one element of the row and one of its neighbour's.
+template <typename T, int VW>
+__device__ __forceinline__ void store_cols(T* row, int c, int N, const Vec<T, VW>& v)
+{
+    if constexpr (VW == 2) {
+        if (c < 0 || c + VW > N) {
+            if (c >= 0 && c < N)
+                row[c] = v.e[0];
+            if (c + 1 >= 0 && c + 1 < N)
+                row[c + 1] = v.e[1];
+            return;
         }
     }
-    float v[NV][VW];
-    float sum = 0.0f;
+    store_vec<T, VW>(row + c, v);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
+{
+    static_assert(BYTES == 16 || BYTES == 4, "cp.async sizes used here");
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+constexpr int THREADS_PER_SM = 512;   // 128 registers a thread, all of shared memory
+
+// Both kernels are persistent: a block (or, TPR = 32, a warp) takes rows r,
+// r + stride, ..., R of them a turn.  Each thread owns the same NV x VW columns
+// (up to 16) of every row.  It copies its own columns of the next turns' rows
+// into its own shared-memory slots (cp.async), so the pipeline needs no
+// barrier; the only ones are the row sums', once a turn, and a turn reads its
+// rows again from shared memory instead of holding them in registers.  A block
+// with a row each and its loads in registers reached 4.5-4.8 TB/s on 8192
+// columns, this form 6.3.
+template <typename T, int VW, int TPR, int NV, int TENSORS>
+struct Shape {
+    static constexpr int THREADS = TPR == 32 ? 256 : TPR;
+    static constexpr int CTAS = THREADS_PER_SM / THREADS;
+    static constexpr int ROWS = THREADS / TPR;
+    static constexpr int SLOT = sizeof(T) * VW;
+    static constexpr int ROW = THREADS * NV * SLOT * TENSORS;   // one row (per warp / block)
+    static constexpr int FIT = 192 * 1024 / CTAS / ROW;         // rows in shared memory
+    static constexpr int R = TPR == 32 ? 1 : FIT >= 8 ? 4 : FIT >= 4 ? 2 : 1;
+    static constexpr int DEPTH = FIT / R > 6 ? 6 : FIT / R;     // turns in the ring
+    static constexpr int RED = ROWS > 1 ? ROWS * TPR * NV * VW * 4 : 0;   // backward: the warps' column sums
+    static constexpr int RING = ROW * R * DEPTH;
+    static constexpr int SMEM = RING > RED ? RING : RED;
+};
+
+// One thread's slots of the ring.
+template <typename T, int VW, int TPR, int NV, int TENSORS>
+struct Ring {
+    using Sh = Shape<T, VW, TPR, NV, TENSORS>;
+    uint8_t* mine;
+    int t, shift, N;
+    int64_t T_, stride;
+
+    __device__ __forceinline__ int col(int i) const { return (i * TPR + t) * VW - shift; }
+    __device__ __forceinline__ Vec<T, VW>* slot(int turn, int k, int tensor, int i) const
+    {
+        return reinterpret_cast<Vec<T, VW>*>(
+            mine + (((turn * Sh::R + k) * TENSORS + tensor) * NV + i) * (Sh::THREADS * Sh::SLOT));
+    }
+    // This thread's columns of a turn's rows of one tensor.  A word that also
+    // holds a neighbouring row's element is copied whole (what does not belong
+    // to the row is masked when it is read), except at the tensor's end.
+    __device__ __forceinline__ void fetch(const T* p, int tensor, int64_t row0, int turn) const
+    {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
+        for (int k = 0; k < Sh::R; ++k) {
+            const int64_t row = row0 + k * stride;
+            if (row >= T_)
+                break;
+            const T* src = p + row * N;
+            const bool end = VW == 2 && row == T_ - 1;
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
-            v[i][j] = 0.0f;
-        if (c < a.N) {
-            if (r != nullptr) {
-                // the norm is of S as it is stored
-#pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    xv[i].e[j] = from_f<T>(to_f(xv[i].e[j]) + to_f(rv[i].e[j]));
-                store_vec<T, VW>(static_cast<T*>(a.S) + row * a.N + c, xv[i]);
-            }
-#pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                v[i][j] = to_f(xv[i].e[j]);
-                sum += v[i][j];
+            for (int i = 0; i < NV; ++i) {
+                const int c = col(i);
+                if (c < N) {
+                    if (VW == 2 && end && c + VW > N)
+                        slot(turn, k, tensor, i)->e[0] = src[c];
+                    else
+                        copy_async<Sh::SLOT>(static_cast<uint32_t>(__cvta_generic_to_shared(slot(turn, k, tensor, i))),
+                                             src + c);
+                }
             }
         }
     }
-    const float inv_n = 1.0f / static_cast<float>(a.N);
-    const float mean = row_sum<TPR>(sum, red[0]) * inv_n;
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-        if (c < a.N) {
-#pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                const float d = v[i][j] - mean;
-                sq = fmaf(d, d, sq);
-            }
-        }
+    // Element j of vector i belongs to the row.
+    __device__ __forceinline__ bool in(int i, int j) const
+    {
+        return VW != 2 || (col(i) + j >= 0 && col(i) + j < N);
     }
-    const float rstd = rsqrtf(row_sum<TPR>(sq, red[1]) * inv_n + a.eps);
-    if (t == 0) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
-    }
+};
+
+__device__ __forceinline__ void commit_copies()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int PENDING>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Sums of R values each over the TPR threads of a row (a warp, or the block).
+// `red` is one of two buffers used in turn: a warp may still read the other.
+template <int TPR, int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float (*red)[TPR <= 32 ? 1 : TPR / 32])
+{
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-        if (c < a.N) {
-            float g[VW], b[VW];
-            load_param<VW>(a.gamma, a.p32, c, 1.0f, a.pvec, g);
-            load_param<VW>(a.beta, a.p32, c, 0.0f, a.pvec, b);
-            Vec<T, VW> y;
+    for (int k = 0; k < R; ++k)
+        v[k] = warp_sum(v[k]);
+    if (TPR > 32) {
+        if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int j = 0; j < VW; ++j)
-                y.e[j] = from_f<T>(fmaf((v[i][j] - mean) * rstd, g[j], b[j]));
-            store_vec<T, VW>(static_cast<T*>(a.Y) + row * a.N + c, y);
+            for (int k = 0; k < R; ++k)
+                red[k][threadIdx.x >> 5] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            v[k] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < TPR / 32; ++w)
+                v[k] += red[k][w];
         }
     }
 }
 
-// Rows too long for registers: one block per row, three passes over the row
+// Forward.  The variance is the exact second pass over (S - mu).
+template <typename T, int VW, int TPR, int NV>
+__global__ void __launch_bounds__(Shape<T, VW, TPR, NV, 2>::THREADS, Shape<T, VW, TPR, NV, 2>::CTAS)
+    norm_fwd_kernel(const FwdArgs a)
+{
+    using Sh = Shape<T, VW, TPR, NV, 2>;
+    constexpr int ROWS = Sh::ROWS, DEPTH = Sh::DEPTH, R = Sh::R;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][R][TPR <= 32 ? 1 : TPR / 32];
+    Ring<T, VW, TPR, NV, 2> ring;
+    ring.mine = smem + threadIdx.x * Sh::SLOT;
+    ring.t = threadIdx.x % TPR;
+    ring.N = static_cast<int>(a.N);
+    ring.T_ = a.T;
+    ring.stride = static_cast<int64_t>(gridDim.x) * ROWS;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR;
+    const T* x = static_cast<const T*>(a.X);
+    const T* r = static_cast<const T*>(a.R);
+    // Rows of one warp or block all start on the same side of a word: the
+    // launch makes the row stride even.
+    ring.shift = row_shift<T, VW>(x, first, a.N);
+    const int N = ring.N;
+    auto fetch = [&](int64_t row0, int turn) {
+        ring.fetch(x, 0, row0, turn);
+        if (r != nullptr)
+            ring.fetch(r, 1, row0, turn);
+        commit_copies();
+    };
+    float g[NV][VW], b[NV][VW];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            g[i][j] = b[i][j] = 0.0f;
+        if (ring.col(i) < N) {
+            load_param<VW>(a.gamma, a.p32, ring.col(i), N, 1.0f, a.pvec, g[i]);
+            load_param<VW>(a.beta, a.p32, ring.col(i), N, 0.0f, a.pvec, b[i]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d)
+        fetch(first + d * R * ring.stride, d);
+    const float inv_n = 1.0f / static_cast<float>(N);
+    int turn = 0;
+    for (int64_t row0 = first; row0 < a.T; row0 += R * ring.stride) {
+        fetch(row0 + (DEPTH - 1) * R * ring.stride, turn == 0 ? DEPTH - 1 : turn - 1);
+        wait_copies<DEPTH - 1>();
+        float mean[R], sq[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = row0 + k * ring.stride;
+            mean[k] = 0.0f;
+            if (row < a.T) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (ring.col(i) < N) {
+                        Vec<T, VW> v = *ring.slot(turn, k, 0, i);
+                        if (r != nullptr) {
+                            // the norm is of S as it is stored
+                            const Vec<T, VW> w = *ring.slot(turn, k, 1, i);
+#pragma unroll
+                            for (int j = 0; j < VW; ++j)
+                                v.e[j] = from_f<T>(to_f(v.e[j]) + to_f(w.e[j]));
+                            *ring.slot(turn, k, 0, i) = v;
+                            store_cols<T, VW>(static_cast<T*>(a.S) + row * a.N, ring.col(i), N, v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < VW; ++j)
+                            mean[k] += ring.in(i, j) ? to_f(v.e[j]) : 0.0f;
+                    }
+                }
+            }
+        }
+        row_sums<TPR, R>(mean, red[0]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] *= inv_n;
+            sq[k] = 0.0f;
+            if (row0 + k * ring.stride < a.T) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (ring.col(i) < N) {
+                        const Vec<T, VW> v = *ring.slot(turn, k, 0, i);
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            const float d = ring.in(i, j) ? to_f(v.e[j]) - mean[k] : 0.0f;
+                            sq[k] = fmaf(d, d, sq[k]);
+                        }
+                    }
+                }
+            }
+        }
+        row_sums<TPR, R>(sq, red[1]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = row0 + k * ring.stride;
+            if (row < a.T) {
+                const float rstd = rsqrtf(sq[k] * inv_n + a.eps);
+                if (ring.t == 0) {
+                    a.mean[row] = mean[k];
+                    a.rstd[row] = rstd;
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (ring.col(i) < N) {
+                        const Vec<T, VW> v = *ring.slot(turn, k, 0, i);
+                        Vec<T, VW> y;
+#pragma unroll
+                        for (int j = 0; j < VW; ++j)
+                            y.e[j] = from_f<T>(fmaf((to_f(v.e[j]) - mean[k]) * rstd, g[i][j], b[i][j]));
+                        store_cols<T, VW>(static_cast<T*>(a.Y) + row * a.N, ring.col(i), N, y);
+                    }
+                }
+            }
+        }
+        turn = turn + 1 == DEPTH ? 0 : turn + 1;
+    }
+    wait_copies<0>();
+}
+
+// Rows that are too long or too badly aligned: one block per row, three passes over it
 // (the second and third mostly from L2).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs a)
@@ -261,8 +427,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs a)
     }
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
         float g[1], b[1];
-        load_param<1>(a.gamma, a.p32, c, 1.0f, false, g);
-        load_param<1>(a.beta, a.p32, c, 0.0f, false, b);
+        load_param<1>(a.gamma, a.p32, c, a.N, 1.0f, false, g);
+        load_param<1>(a.beta, a.p32, c, a.N, 0.0f, false, b);
         static_cast<T*>(a.Y)[row * a.N + c] = from_f<T>(fmaf((to_f(in[c]) - mean) * rstd, g[0], b[0]));
     }
 }
@@ -277,221 +443,153 @@ struct BwdArgs {
     int p32, pvec;
 };
 
-constexpr int BWD_THREADS_PER_SM = 512;   // 128 registers a thread: 32 column sums, 16 gammas, a row's values
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
-{
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES < 4 ? 4 : BYTES)
-                     : "memory");
-}
-
-// Persistent: a block (or, TPR = 32, a warp) takes rows r, r + stride, ...
-// Each thread owns the same NV x VW columns of every row and keeps their two
-// sums in registers.  It copies its own columns of the rows ahead into its own
-// shared-memory slots (cp.async, DEPTH rows in flight), so the pipeline needs
-// no barrier; the only one per row is the row sums'.
+// Backward: beside the rows each thread keeps the two sums of its columns.
 template <typename T, int VW, int TPR, int NV>
-struct BwdShape {
-    static constexpr int THREADS = TPR == 32 ? 256 : TPR;
-    static constexpr int CTAS = BWD_THREADS_PER_SM / THREADS;
-    static constexpr int ROWS = THREADS / TPR;
-    static constexpr int SLOT = sizeof(T) * VW < 4 ? 4 : sizeof(T) * VW;
-    static constexpr int STAGE = THREADS * NV * SLOT * 3;       // dY, S, dS of one row (per warp / block)
-    static constexpr int FIT = 192 * 1024 / CTAS / STAGE;
-    static constexpr int DEPTH = FIT > 4 ? 4 : FIT;
-    static constexpr int RED = ROWS > 1 ? ROWS * TPR * NV * VW * 4 : 0;   // the warps' column sums at the end
-    static constexpr int RING = STAGE * DEPTH;
-    static constexpr int SMEM = RING > RED ? RING : RED;
-};
-
-template <typename T, int VW, int TPR, int NV>
-__global__ void __launch_bounds__(BwdShape<T, VW, TPR, NV>::THREADS, BwdShape<T, VW, TPR, NV>::CTAS)
+__global__ void __launch_bounds__(Shape<T, VW, TPR, NV, 3>::THREADS, Shape<T, VW, TPR, NV, 3>::CTAS)
     norm_bwd_kernel(const BwdArgs a)
 {
-    using Sh = BwdShape<T, VW, TPR, NV>;
-    constexpr int THREADS = Sh::THREADS, ROWS = Sh::ROWS, DEPTH = Sh::DEPTH, SLOT = Sh::SLOT;
-    constexpr bool ASYNC = sizeof(T) * VW >= 4;   // cp.async copies at least 4 bytes
+    using Sh = Shape<T, VW, TPR, NV, 3>;
+    constexpr int THREADS = Sh::THREADS, ROWS = Sh::ROWS, DEPTH = Sh::DEPTH, R = Sh::R;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 red[2][TPR <= 32 ? 1 : TPR / 32];
-    const int t = threadIdx.x % TPR;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * ROWS;
+    __shared__ float red[2][2 * R][TPR <= 32 ? 1 : TPR / 32];
+    Ring<T, VW, TPR, NV, 3> ring;
+    ring.mine = smem + threadIdx.x * Sh::SLOT;
+    ring.t = threadIdx.x % TPR;
+    ring.N = static_cast<int>(a.N);
+    ring.T_ = a.T;
+    ring.stride = static_cast<int64_t>(gridDim.x) * ROWS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR;
-    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * SLOT;
     const T* dy_p = static_cast<const T*>(a.dY);
     const T* s_p = static_cast<const T*>(a.S);
     const T* ds_p = static_cast<const T*>(a.dS);
-
-    auto slot = [&](int stage, int tensor, int i) -> uint32_t {
-        return static_cast<uint32_t>(((stage * 3 + tensor) * NV + i) * (THREADS * SLOT));
+    ring.shift = row_shift<T, VW>(s_p, first, a.N);   // the same for all of its rows: the stride is even
+    const int N = ring.N;
+    auto fetch = [&](int64_t row0, int turn) {
+        ring.fetch(dy_p, 0, row0, turn);
+        ring.fetch(s_p, 1, row0, turn);
+        if (ds_p != nullptr)
+            ring.fetch(ds_p, 2, row0, turn);
+        commit_copies();
     };
-    auto fetch = [&](int64_t row, int stage) {
-        if (row < a.T) {
+    float g[NV][VW], sum_g[NV][VW], sum_b[NV][VW];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-                if (c < a.N) {
-                    const int64_t at = row * a.N + c;
-                    if (ASYNC) {
-                        copy_async<sizeof(T) * VW>(slot0 + slot(stage, 0, i), dy_p + at);
-                        copy_async<sizeof(T) * VW>(slot0 + slot(stage, 1, i), s_p + at);
-                        if (ds_p != nullptr)
-                            copy_async<sizeof(T) * VW>(slot0 + slot(stage, 2, i), ds_p + at);
-                    } else {
-                        uint8_t* q = smem + threadIdx.x * SLOT;
-                        const Vec<T, VW> d = load_stream<T, VW>(dy_p + at), x = load_stream<T, VW>(s_p + at);
-                        *reinterpret_cast<Vec<T, VW>*>(q + slot(stage, 0, i)) = d;
-                        *reinterpret_cast<Vec<T, VW>*>(q + slot(stage, 1, i)) = x;
-                        if (ds_p != nullptr)
-                            *reinterpret_cast<Vec<T, VW>*>(q + slot(stage, 2, i)) = load_stream<T, VW>(ds_p + at);
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            g[i][j] = sum_g[i][j] = sum_b[i][j] = 0.0f;
+        if (ring.col(i) < N)
+            load_param<VW>(a.gamma, a.p32, ring.col(i), N, 1.0f, a.pvec, g[i]);
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d)
+        fetch(first + d * R * ring.stride, d);
+    const float inv_n = 1.0f / static_cast<float>(N);
+    int turn = 0, par = 0;
+    float mean[R], rstd[R];
+    auto stats = [&](int64_t row0, float (&m)[R], float (&r)[R]) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = row0 + k * ring.stride;
+            m[k] = row < a.T ? __ldg(a.mean + row) : 0.0f;
+            r[k] = row < a.T ? __ldg(a.rstd + row) : 0.0f;
+        }
+    };
+    stats(first, mean, rstd);
+    for (int64_t row0 = first; row0 < a.T; row0 += R * ring.stride) {
+        fetch(row0 + (DEPTH - 1) * R * ring.stride, turn == 0 ? DEPTH - 1 : turn - 1);
+        float mean_n[R], rstd_n[R];
+        stats(row0 + R * ring.stride, mean_n, rstd_n);
+        wait_copies<DEPTH - 1>();
+        float c[2 * R];   // sums of g and of g xh of each row
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            c[2 * k] = c[2 * k + 1] = 0.0f;
+            if (row0 + k * ring.stride < a.T) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (ring.col(i) < N) {
+                        const Vec<T, VW> d = *ring.slot(turn, k, 0, i), s = *ring.slot(turn, k, 1, i);
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            const float dy = ring.in(i, j) ? to_f(d.e[j]) : 0.0f;
+                            const float xh = ring.in(i, j) ? (to_f(s.e[j]) - mean[k]) * rstd[k] : 0.0f;
+                            sum_g[i][j] = fmaf(dy, xh, sum_g[i][j]);
+                            sum_b[i][j] += dy;
+                            const float gy = dy * g[i][j];
+                            c[2 * k] += gy;
+                            c[2 * k + 1] = fmaf(gy, xh, c[2 * k + 1]);
+                        }
                     }
                 }
             }
         }
-        if (ASYNC)
-            asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    auto slot_vec = [&](int stage, int tensor, int i) -> Vec<T, VW> {
-        return *reinterpret_cast<const Vec<T, VW>*>(smem + threadIdx.x * SLOT + slot(stage, tensor, i));
-    };
-
-    float g[NV][VW], sum_g[NV][VW], sum_b[NV][VW];
+        row_sums<TPR, 2 * R>(c, red[par]);
+        par ^= 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = row0 + k * ring.stride;
+            if (row < a.T) {
+                const float m1 = c[2 * k] * inv_n, m2 = c[2 * k + 1] * inv_n;
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
-            g[i][j] = sum_g[i][j] = sum_b[i][j] = 0.0f;
-        if (c < a.N)
-            load_param<VW>(a.gamma, a.p32, c, 1.0f, a.pvec, g[i]);
-    }
+                for (int i = 0; i < NV; ++i) {
+                    if (ring.col(i) < N) {
+                        const Vec<T, VW> d = *ring.slot(turn, k, 0, i), s = *ring.slot(turn, k, 1, i);
+                        Vec<T, VW> e, o;
+                        if (ds_p != nullptr)
+                            e = *ring.slot(turn, k, 2, i);
 #pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d)
-        fetch(first + d * stride, d);
-
-    const float inv_n = 1.0f / static_cast<float>(a.N);
-    int stage = 0, par = 0;
-    float mean = 0.0f, rstd = 0.0f;
-    if (first < a.T) {
-        mean = __ldg(a.mean + first);
-        rstd = __ldg(a.rstd + first);
-    }
-    for (int64_t row = first; row < a.T; row += stride) {
-        const int64_t ahead = row + (DEPTH - 1) * stride;
-        fetch(ahead, stage == 0 ? DEPTH - 1 : stage - 1);
-        const int64_t next = row + stride;
-        float mean_n = 0.0f, rstd_n = 0.0f;
-        if (next < a.T) {
-            mean_n = __ldg(a.mean + next);
-            rstd_n = __ldg(a.rstd + next);
-        }
-        if (ASYNC)
-            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-        float xh[NV][VW], gy[NV][VW];
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-#pragma unroll
-            for (int j = 0; j < VW; ++j)
-                xh[i][j] = gy[i][j] = 0.0f;
-            if (c < a.N) {
-                const Vec<T, VW> d = slot_vec(stage, 0, i), s = slot_vec(stage, 1, i);
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    const float dy = to_f(d.e[j]);
-                    xh[i][j] = (to_f(s.e[j]) - mean) * rstd;
-                    sum_g[i][j] = fmaf(dy, xh[i][j], sum_g[i][j]);
-                    sum_b[i][j] += dy;
-                    gy[i][j] = dy * g[i][j];
-                    c1 += gy[i][j];
-                    c2 = fmaf(gy[i][j], xh[i][j], c2);
+                        for (int j = 0; j < VW; ++j) {
+                            const float xh = (to_f(s.e[j]) - mean[k]) * rstd[k];
+                            const float v = fmaf(-xh, m2, fmaf(to_f(d.e[j]), g[i][j], -m1));
+                            o.e[j] = from_f<T>(ds_p != nullptr ? fmaf(rstd[k], v, to_f(e.e[j])) : rstd[k] * v);
+                        }
+                        store_cols<T, VW>(static_cast<T*>(a.dX) + row * a.N, ring.col(i), N, o);
+                    }
                 }
             }
+            mean[k] = mean_n[k];
+            rstd[k] = rstd_n[k];
         }
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
-        if (TPR > 32) {
-            // two buffers: a warp may still read one while the next row's sums are written
-            if ((threadIdx.x & 31) == 0)
-                red[par][threadIdx.x >> 5] = make_float2(c1, c2);
-            __syncthreads();
-            c1 = c2 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) {
-                const float2 v = red[par][w];
-                c1 += v.x;
-                c2 += v.y;
-            }
-            par ^= 1;
-        }
-        c1 *= inv_n;
-        c2 *= inv_n;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-            if (c < a.N) {
-                Vec<T, VW> o;
-                float add[VW];
-#pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    add[j] = 0.0f;
-                if (ds_p != nullptr) {
-                    const Vec<T, VW> e = slot_vec(stage, 2, i);
-#pragma unroll
-                    for (int j = 0; j < VW; ++j)
-                        add[j] = to_f(e.e[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    o.e[j] = from_f<T>(fmaf(rstd, fmaf(-xh[i][j], c2, gy[i][j] - c1), add[j]));
-                store_vec<T, VW>(static_cast<T*>(a.dX) + row * a.N + c, o);
-            }
-        }
-        mean = mean_n;
-        rstd = rstd_n;
-        stage = stage + 1 == DEPTH ? 0 : stage + 1;
+        turn = turn + 1 == DEPTH ? 0 : turn + 1;
     }
-    if (ASYNC)
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    wait_copies<0>();
     if (a.partial == nullptr)
         return;
     float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
     if (ROWS == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = static_cast<int64_t>(i * TPR + t) * VW;
-            if (c < a.N) {
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    out[c + j] = sum_g[i][j];
-                    out[a.N + c + j] = sum_b[i][j];
+            for (int j = 0; j < VW; ++j) {
+                const int at = ring.col(i) + j;
+                if (at >= 0 && at < N) {
+                    out[at] = sum_g[i][j];
+                    out[a.N + at] = sum_b[i][j];
                 }
             }
-        }
         return;
     }
     // several warps per block: their sums meet in shared memory, warp order
     float* acc = reinterpret_cast<float*>(smem);
-    const int span = TPR * NV * VW;
+    constexpr int span = TPR * NV * VW;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VW; ++j)
-                acc[(threadIdx.x / TPR) * span + (i * TPR + t) * VW + j] = which ? sum_b[i][j] : sum_g[i][j];
+            for (int j = 0; j < VW; ++j) {
+                const int at = ring.col(i) + j;
+                if (at >= 0 && at < N)
+                    acc[(threadIdx.x / TPR) * span + at] = which ? sum_b[i][j] : sum_g[i][j];
+            }
         __syncthreads();
-        for (int64_t c = threadIdx.x; c < a.N; c += THREADS) {
+        for (int at = threadIdx.x; at < N; at += THREADS) {
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < ROWS; ++w)
-                v += acc[w * span + c];
-            out[which * a.N + c] = v;
+                v += acc[w * span + at];
+            out[which * a.N + at] = v;
         }
     }
 }
@@ -519,7 +617,7 @@ __global__ void __launch_bounds__(512) norm_sums_kernel(const float* partial, in
     }
 }
 
-// Rows too long for a block's registers: dX by one block per row (two passes),
+// Rows that are too long or too badly aligned: dX by one block per row (two passes),
 // the column sums by a second sweep.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdArgs a)
@@ -532,7 +630,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdArgs a)
     float c1 = 0.0f, c2 = 0.0f;
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
         float g[1];
-        load_param<1>(a.gamma, a.p32, c, 1.0f, false, g);
+        load_param<1>(a.gamma, a.p32, c, a.N, 1.0f, false, g);
         const float gy = to_f(dy[c]) * g[0];
         c1 += gy;
         c2 = fmaf(gy, (to_f(s[c]) - mean) * rstd, c2);
@@ -542,7 +640,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdArgs a)
     c2 = row_sum<1024>(c2, red[1]) * inv_n;
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
         float g[1];
-        load_param<1>(a.gamma, a.p32, c, 1.0f, false, g);
+        load_param<1>(a.gamma, a.p32, c, a.N, 1.0f, false, g);
         const float add = a.dS == nullptr ? 0.0f : to_f(static_cast<const T*>(a.dS)[row * a.N + c]);
         const float xh = (to_f(s[c]) - mean) * rstd;
         static_cast<T*>(a.dX)[row * a.N + c] =
@@ -571,81 +669,88 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const BwdArgs a, int 
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// A persistent kernel's launch; its shared memory is asked for once.
+template <typename Args>
+int launch(void (*kernel)(Args), bool& ready, int ctas, int threads, int smem, const Args& a, cudaStream_t s)
+{
+    if (!ready && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return -1;
+    ready = true;
+    kernel<<<ctas, threads, smem, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
 template <typename T, int VW, int TPR, int NV>
-int fwd(const FwdArgs& a, cudaStream_t s)
+int fwd(const FwdArgs& a, int ctas, cudaStream_t s)
 {
-    constexpr int threads = TPR < 128 ? 128 : TPR;
-    constexpr int rows = threads / TPR;
-    norm_fwd_kernel<T, VW, TPR, NV><<<static_cast<unsigned>((a.T + rows - 1) / rows), threads, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
-}
-
-// Threads and vectors per row by the row's vectors: a warp up to 128 vectors
-// (no block barrier), then blocks of four vectors a thread.
-template <typename T, int VW>
-int fwd_any(const FwdArgs& a, cudaStream_t s)
-{
-    const int64_t v = (a.N + VW - 1) / VW;
-    if (v <= 32)
-        return fwd<T, VW, 32, 1>(a, s);
-    if (v <= 64)
-        return fwd<T, VW, 32, 2>(a, s);
-    if (v <= 128)
-        return fwd<T, VW, 32, 4>(a, s);
-    if (v <= 256)
-        return fwd<T, VW, 128, 2>(a, s);
-    if (v <= 512)
-        return fwd<T, VW, 128, 4>(a, s);
-    if (v <= 1024)
-        return fwd<T, VW, 256, 4>(a, s);
-    if (v <= 2048)
-        return fwd<T, VW, 512, 4>(a, s);
-    if (v <= 4096)
-        return fwd<T, VW, 1024, 4>(a, s);
-    if (VW <= 2 && v <= 8192)
-        return fwd<T, VW <= 2 ? VW : 1, 1024, 8>(a, s);
-    norm_fwd_long_kernel<T><<<static_cast<unsigned>(a.T), 1024, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
-}
-
-// Columns a block of 512 threads holds 16 of in each thread's registers.
-constexpr int64_t BWD_MAX_N = 8192;
-
-// (threads per row, rows per CTA, CTAs per SM) of a width: one rule for every
-// type, so that the workspace can be sized without knowing it.
-void bwd_shape(int64_t N, int& tpr, int& ctas_per_sm)
-{
-    tpr = N <= 512 ? 32 : N <= 2048 ? 128 : N <= 4096 ? 256 : 512;
-    ctas_per_sm = BWD_THREADS_PER_SM / (tpr == 32 ? 256 : tpr);
+    using Sh = Shape<T, VW, TPR, NV, 2>;
+    static_assert(Sh::DEPTH >= 2, "two turns in shared memory");
+    static bool ready = false;
+    return launch(norm_fwd_kernel<T, VW, TPR, NV>, ready, ctas, Sh::THREADS, Sh::SMEM, a, s);
 }
 
 template <typename T, int VW, int TPR, int NV>
 int bwd(const BwdArgs& a, int ctas, cudaStream_t s)
 {
-    using Sh = BwdShape<T, VW, TPR, NV>;
-    static_assert(TPR * NV * VW <= BWD_MAX_N && Sh::DEPTH >= 2, "a row fits, two rows in flight");
-    if (cudaFuncSetAttribute(norm_bwd_kernel<T, VW, TPR, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Sh::SMEM) != cudaSuccess)
-        return -1;
-    norm_bwd_kernel<T, VW, TPR, NV><<<ctas, Sh::THREADS, Sh::SMEM, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    using Sh = Shape<T, VW, TPR, NV, 3>;
+    static_assert(Sh::DEPTH >= 2, "two turns in shared memory");
+    static bool ready = false;
+    return launch(norm_bwd_kernel<T, VW, TPR, NV>, ready, ctas, Sh::THREADS, Sh::SMEM, a, s);
 }
 
-template <typename T, int VW>
-int bwd_any(const BwdArgs& a, int ctas, cudaStream_t s)
+// Longest row of the persistent kernels: 16 columns for each of 512 threads.
+constexpr int64_t MAX_N = 8192;
+
+// Threads per row of a width (rows of odd length may need a column more, see
+// row_shift): one rule for every type, so that the workspace can be sized
+// without knowing it.
+int row_threads(int64_t N)
 {
-    constexpr int F = 16 / VW;   // vectors of 16 columns
-    if (a.N <= 256)
-        return bwd<T, VW, 32, F / 2>(a, ctas, s);
-    if (a.N <= 512)
-        return bwd<T, VW, 32, F>(a, ctas, s);
-    if (a.N <= 1024)
-        return bwd<T, VW, 128, F / 2>(a, ctas, s);
-    if (a.N <= 2048)
-        return bwd<T, VW, 128, F>(a, ctas, s);
-    if (a.N <= 4096)
-        return bwd<T, VW, 256, F>(a, ctas, s);
-    return bwd<T, VW, 512, F>(a, ctas, s);
+    const int64_t n = N + (N & 1);
+    return n <= 512 ? 32 : n <= 1024 ? 128 : n <= 2048 ? 256 : 512;
+}
+
+#define TFFN_NORM_ANY(NAME, ARGS)                                                              \
+    template <typename T, int VW>                                                              \
+    int NAME##_any(const ARGS& a, int ctas, cudaStream_t s)                                    \
+    {                                                                                          \
+        constexpr int F = 16 / VW; /* vectors of 16 columns */                                 \
+        const int64_t n = a.N + (a.N & 1);                                                     \
+        switch (row_threads(a.N)) {                                                        \
+        case 32: return n <= 256 ? NAME<T, VW, 32, F / 2>(a, ctas, s) : NAME<T, VW, 32, F>(a, ctas, s); \
+        case 128: return NAME<T, VW, 128, F / 2>(a, ctas, s);                                  \
+        case 256: return NAME<T, VW, 256, F / 2>(a, ctas, s);                                  \
+        default: return n <= 4096 ? NAME<T, VW, 512, F / 2>(a, ctas, s) : NAME<T, VW, 512, F>(a, ctas, s); \
+        }                                                                                      \
+    }
+TFFN_NORM_ANY(fwd, FwdArgs)
+TFFN_NORM_ANY(bwd, BwdArgs)
+#undef TFFN_NORM_ANY
+
+// CTAs of the persistent kernels: one wave of them, no more than there are
+// rows.  Even: rows of odd length keep their side of a word from turn to turn.
+int row_ctas(int64_t T, int64_t N, int sms)
+{
+    const int tpr = row_threads(N);
+    const int64_t per_sm = THREADS_PER_SM / (tpr == 32 ? 256 : tpr), rows = tpr == 32 ? 8 : 1;
+    const int64_t ctas = std::min<int64_t>((T + rows - 1) / rows, int64_t(sms) * per_sm);
+    return static_cast<int>((ctas + 1) / 2 * 2);
+}
+
+// How the persistent kernels take a call: vectors of 16 bytes, else 4-byte
+// words (bf16 tensors of odd rows all starting on the same side of a word), else
+// not at all.
+enum class Access { VEC, WORD, ELEMENT };
+template <class... P>
+Access access(bool f32, int64_t N, const P*... p)
+{
+    const uintptr_t e = f32 ? 4 : 2;
+    const uintptr_t all = (reinterpret_cast<uintptr_t>(p) | ...);
+    if (N > MAX_N)
+        return Access::ELEMENT;
+    if ((static_cast<uintptr_t>(N) * e) % 16 == 0 && all % 16 == 0)
+        return Access::VEC;
+    return all % 4 == 0 ? Access::WORD : Access::ELEMENT;
 }
 
 }  // namespace norm
@@ -653,68 +758,59 @@ int bwd_any(const BwdArgs& a, int ctas, cudaStream_t s)
 int launch_norm_fwd(const NormFwd& n, int sms, cudaStream_t s)
 {
     using namespace norm;
-    (void)sms;
+    using B = __nv_bfloat16;
     FwdArgs a{n.X, n.R, n.gamma, n.beta, n.Y, n.S, n.mean, n.rstd, n.T, n.N, n.eps, n.p32 ? 1 : 0, 0};
     a.pvec = aligned_to(n.gamma, 16) && aligned_to(n.beta, 16) ? 1 : 0;
-    const size_t e = n.f32 ? 4 : 2;
-    auto fits = [&](size_t bytes) {   // every row of every tensor starts on a multiple of `bytes`
-        return (n.N * e) % bytes == 0 && aligned_to(n.X, bytes) && aligned_to(n.R, bytes) && aligned_to(n.Y, bytes) &&
-               aligned_to(n.S, bytes);
-    };
-    if (n.f32)
-        return fits(16) ? fwd_any<float, 4>(a, s) : fwd_any<float, 1>(a, s);
-    if (fits(16))
-        return fwd_any<__nv_bfloat16, 8>(a, s);
-    return fits(4) ? fwd_any<__nv_bfloat16, 2>(a, s) : fwd_any<__nv_bfloat16, 1>(a, s);
+    const int ctas = row_ctas(n.T, n.N, sms);
+    switch (access(n.f32, n.N, n.X, n.R, static_cast<const void*>(n.Y), static_cast<const void*>(n.S))) {
+    case Access::VEC: return n.f32 ? fwd_any<float, 4>(a, ctas, s) : fwd_any<B, 8>(a, ctas, s);
+    case Access::WORD: return n.f32 ? fwd_any<float, 1>(a, ctas, s) : fwd_any<B, 2>(a, ctas, s);
+    default:
+        if (n.f32)
+            norm_fwd_long_kernel<float><<<static_cast<unsigned>(a.T), 1024, 0, s>>>(a);
+        else
+            norm_fwd_long_kernel<B><<<static_cast<unsigned>(a.T), 1024, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    }
 }
 
+// CTAs whose column sums a backward pass keeps: enough for either way of
+// running it (persistent CTAs, or the row chunks of a column sweep).
 int norm_bwd_ctas(int64_t T, int64_t N, int sms)
 {
     using namespace norm;
-    if (N > BWD_MAX_N)   // row chunks of the column sweep
-        return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, (T + 31) / 32)));
-    int tpr = 0, per_sm = 0;
-    bwd_shape(N, tpr, per_sm);
-    const int rows = tpr == 32 ? 8 : 1;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + rows - 1) / rows, int64_t(sms) * per_sm)));
+    const int chunks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, (T + 31) / 32)));
+    return N > MAX_N ? chunks : std::max(chunks, row_ctas(T, N, sms));
 }
 
 int launch_norm_bwd(const NormBwd& n, int sms, cudaStream_t s)
 {
     using namespace norm;
-    const int ctas = norm_bwd_ctas(n.T, n.N, sms);
+    using B = __nv_bfloat16;
+    int ctas = row_ctas(n.T, n.N, sms);
     BwdArgs a{n.dY, n.S, n.gamma, n.dS, n.mean, n.rstd, n.dX, n.dgamma ? n.partial : nullptr, n.T, n.N,
               n.p32 ? 1 : 0, aligned_to(n.gamma, 16) ? 1 : 0};
-    int launches = 1;
-    if (n.N > BWD_MAX_N) {
+    int launches = 1, rc = 0;
+    switch (access(n.f32, n.N, n.dY, n.S, n.dS, static_cast<const void*>(n.dX))) {
+    case Access::VEC: rc = n.f32 ? bwd_any<float, 4>(a, ctas, s) : bwd_any<B, 8>(a, ctas, s); break;
+    case Access::WORD: rc = n.f32 ? bwd_any<float, 1>(a, ctas, s) : bwd_any<B, 2>(a, ctas, s); break;
+    default:
         if (n.f32)
             norm_bwd_long_kernel<float><<<static_cast<unsigned>(n.T), 1024, 0, s>>>(a);
         else
-            norm_bwd_long_kernel<__nv_bfloat16><<<static_cast<unsigned>(n.T), 1024, 0, s>>>(a);
+            norm_bwd_long_kernel<B><<<static_cast<unsigned>(n.T), 1024, 0, s>>>(a);
         if (n.dgamma) {
+            ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, (n.T + 31) / 32)));
             const dim3 grid(static_cast<unsigned>((n.N + 127) / 128), static_cast<unsigned>(ctas));
             if (n.f32)
                 norm_columns_kernel<float><<<grid, 128, 0, s>>>(a, ctas);
             else
-                norm_columns_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a, ctas);
+                norm_columns_kernel<B><<<grid, 128, 0, s>>>(a, ctas);
             ++launches;
         }
-    } else {
-        const size_t e = n.f32 ? 4 : 2;
-        auto fits = [&](size_t bytes) {
-            return (n.N * e) % bytes == 0 && aligned_to(n.dY, bytes) && aligned_to(n.S, bytes) &&
-                   aligned_to(n.dS, bytes) && aligned_to(n.dX, bytes);
-        };
-        int rc;
-        if (n.f32)
-            rc = fits(16) ? bwd_any<float, 4>(a, ctas, s) : bwd_any<float, 1>(a, ctas, s);
-        else if (fits(16))
-            rc = bwd_any<__nv_bfloat16, 8>(a, ctas, s);
-        else
-            rc = fits(4) ? bwd_any<__nv_bfloat16, 2>(a, ctas, s) : bwd_any<__nv_bfloat16, 1>(a, ctas, s);
-        if (rc != 0)
-            return -1;
     }
+    if (rc != 0)
+        return -1;
     if (n.dgamma) {
         const dim3 grid(static_cast<unsigned>((n.N + 31) / 32), 2);
         norm_sums_kernel<<<grid, 512, 0, s>>>(n.partial, ctas, n.N, n.dgamma, n.dbeta);
