@@ -186,7 +186,7 @@ struct Shape {
     static constexpr int SLOT = sizeof(T) * VW;
     static constexpr int ROW = THREADS * NV * SLOT * TENSORS;   // one row (per warp / block)
     static constexpr int FIT = 192 * 1024 / CTAS / ROW;         // rows in shared memory
-    static constexpr int R = TPR == 32 ? 1 : FIT >= 8 ? 4 : FIT >= 4 ? 2 : 1;
+    static constexpr int R = TPR == 32 ? 1 : FIT >= 4 ? 2 : 1;
     static constexpr int DEPTH = FIT / R > 6 ? 6 : FIT / R;     // turns in the ring
     static constexpr int RED = ROWS > 1 ? ROWS * TPR * NV * VW * 4 : 0;   // backward: the warps' column sums
     static constexpr int RING = ROW * R * DEPTH;
@@ -707,7 +707,7 @@ constexpr int64_t MAX_N = 8192;
 int row_threads(int64_t N)
 {
     const int64_t n = N + (N & 1);
-    return n <= 512 ? 32 : n <= 1024 ? 128 : n <= 2048 ? 256 : 512;
+    return n <= 512 ? 32 : n <= 2048 ? 128 : n <= 4096 ? 256 : 512;
 }
 
 #define TFFN_NORM_ANY(NAME, ARGS)                                                              \
@@ -718,9 +718,9 @@ int row_threads(int64_t N)
         const int64_t n = a.N + (a.N & 1);                                                     \
         switch (row_threads(a.N)) {                                                        \
         case 32: return n <= 256 ? NAME<T, VW, 32, F / 2>(a, ctas, s) : NAME<T, VW, 32, F>(a, ctas, s); \
-        case 128: return NAME<T, VW, 128, F / 2>(a, ctas, s);                                  \
-        case 256: return NAME<T, VW, 256, F / 2>(a, ctas, s);                                  \
-        default: return n <= 4096 ? NAME<T, VW, 512, F / 2>(a, ctas, s) : NAME<T, VW, 512, F>(a, ctas, s); \
+        case 128: return n <= 1024 ? NAME<T, VW, 128, F / 2>(a, ctas, s) : NAME<T, VW, 128, F>(a, ctas, s); \
+        case 256: return NAME<T, VW, 256, F>(a, ctas, s);                                      \
+        default: return NAME<T, VW, 512, F>(a, ctas, s);                                       \
         }                                                                                      \
     }
 TFFN_NORM_ANY(fwd, FwdArgs)
