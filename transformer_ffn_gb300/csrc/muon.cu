@@ -23,9 +23,27 @@ struct alignas(16) Vec {
     T e[W];
 };
 
+// A thread's sum of squares in fp32: values past 2^40, whose squares could leave
+// fp32's range, are added 2^-80 times themselves (squares below fp32's range do
+// not matter beside the 1e-7 that the norm is added to).
+struct Squares {
+    float small = 0.0f, large = 0.0f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const bool big = fabsf(x) > 0x1p40f;
+        const float y = big ? x * 0x1p-80f : x;
+        const float q = y * y;
+        small += big ? 0.0f : q;
+        large += big ? q : 0.0f;
+    }
+    __device__ __forceinline__ double sum() const
+    {
+        return static_cast<double>(small) + static_cast<double>(large) * 0x1p160;
+    }
+};
+
 // Sums of squares of one entry's `elems` values: part[entry][block].  A thread
-// adds in fp32 over its own few thousand values, threads are joined in fp64
-// (the sum of a large matrix can pass fp32's range only there).
+// adds in fp32 over its own few thousand values, threads are joined in fp64.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) muon_norm_kernel(const T* G, int64_t elems, double* part)
 {
@@ -39,7 +57,7 @@ __global__ void __launch_bounds__(THREADS) muon_norm_kernel(const T* G, int64_t 
     const int64_t head = mis == 0 ? 0 : (W - mis < elems ? W - mis : elems);
     const int64_t vecs = (elems - head) / W;
     const Vec<T>* v = reinterpret_cast<const Vec<T>*>(g + head);
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    Squares s[4];
     int64_t i = id;
     for (; i + 3 * step < vecs; i += 4 * step) {
         Vec<T> x[4];
@@ -50,20 +68,19 @@ __global__ void __launch_bounds__(THREADS) muon_norm_kernel(const T* G, int64_t 
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                s[k] = fmaf(to_f(x[k].e[j]), to_f(x[k].e[j]), s[k]);
+                s[k].add(to_f(x[k].e[j]));
     }
     for (; i < vecs; i += step) {
         const Vec<T> x = v[i];
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            s[0] = fmaf(to_f(x.e[j]), to_f(x.e[j]), s[0]);
+            s[0].add(to_f(x.e[j]));
     }
     const int64_t tail = head + vecs * W;
     for (int64_t k = id; k < head + (elems - tail); k += step) {
-        const float x = to_f(k < head ? g[k] : g[tail + k - head]);
-        s[1] = fmaf(x, x, s[1]);
+        s[1].add(to_f(k < head ? g[k] : g[tail + k - head]));
     }
-    double d = static_cast<double>(s[0]) + s[1] + s[2] + s[3];
+    double d = s[0].sum() + s[1].sum() + s[2].sum() + s[3].sum();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         d += __shfl_xor_sync(0xffffffffu, d, o);
@@ -85,7 +102,7 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
                                                             int vec)
 {
     __shared__ double red[THREADS / 32];
-    __shared__ float factor;
+    __shared__ float factor, before;
     const T* g = G + blockIdx.y * m * n;
     __half* x = X + blockIdx.y * m * ld;
     double d = 0.0;
@@ -101,10 +118,15 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
         d = 0.0;
         for (int k = 0; k < THREADS / 32; ++k)
             d += red[k];
-        factor = static_cast<float>(static_cast<double>(scale) / (sqrt(d) + static_cast<double>(eps)));
+        // X = (G before) factor: a norm past 2^60 is first brought down, so that
+        // neither number leaves fp32's normal range
+        const double norm = sqrt(d) + static_cast<double>(eps);
+        const double pre = norm > 0x1p60 ? 0x1p-60 : 1.0;
+        before = static_cast<float>(pre);
+        factor = static_cast<float>(static_cast<double>(scale) / (norm * pre));
     }
     __syncthreads();
-    const float f = factor;
+    const float f = factor, f0 = before;
     const int64_t per_row = ld / 8;
     const int64_t total = m * per_row;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < total;
@@ -129,7 +151,7 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
         __half2 o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            o[j] = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
+            o[j] = __floats2half2_rn(v[2 * j] * f0 * f, v[2 * j + 1] * f0 * f);
         *reinterpret_cast<uint4*>(x + r * ld + c) = *reinterpret_cast<const uint4*>(o);
     }
 }

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Shape<T, VW, TPR, NV, 2>::THREADS, Shape<T, VW
 #pragma unroll
     for (int d = 0; d < DEPTH - 1; ++d)
         fetch(first + d * R * ring.stride, d);
-    const float inv_n = 1.0f / static_cast<float>(N);
+    const float n = static_cast<float>(N);
     int turn = 0;
     for (int64_t row0 = first; row0 < a.T; row0 += R * ring.stride) {
         fetch(row0 + (DEPTH - 1) * R * ring.stride, turn == 0 ? DEPTH - 1 : turn - 1);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(Shape<T, VW, TPR, NV, 2>::THREADS, Shape<T, VW
         row_sums<TPR, R>(mean, red[0]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            mean[k] *= inv_n;
+            mean[k] = mean[k] / n;   // a division: the mean of equal values is that value
             sq[k] = 0.0f;
             if (row0 + k * ring.stride < a.T) {
 #pragma unroll
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(Shape<T, VW, TPR, NV, 2>::THREADS, Shape<T, VW
         for (int k = 0; k < R; ++k) {
             const int64_t row = row0 + k * ring.stride;
             if (row < a.T) {
-                const float rstd = rsqrtf(sq[k] * inv_n + a.eps);
+                const float rstd = rsqrtf(sq[k] / n + a.eps);
                 if (ring.t == 0) {
                     a.mean[row] = mean[k];
                     a.rstd[row] = rstd;
@@ -413,14 +413,14 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs a)
         sum += to_f(v);
     }
     const T* in = r != nullptr ? s : x;   // each thread reads back what it wrote itself
-    const float inv_n = 1.0f / static_cast<float>(a.N);
-    const float mean = row_sum<1024>(sum, red[0]) * inv_n;
+    const float n = static_cast<float>(a.N);
+    const float mean = row_sum<1024>(sum, red[0]) / n;
     float sq = 0.0f;
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
         const float d = to_f(in[c]) - mean;
         sq = fmaf(d, d, sq);
     }
-    const float rstd = rsqrtf(row_sum<1024>(sq, red[1]) * inv_n + a.eps);
+    const float rstd = rsqrtf(row_sum<1024>(sq, red[1]) / n + a.eps);
     if (threadIdx.x == 0) {
         a.mean[row] = mean;
         a.rstd[row] = rstd;
