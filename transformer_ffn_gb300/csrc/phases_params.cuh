@@ -12,7 +12,7 @@ using engine::BM;
 
 constexpr int EPI_WARPS = 8;                           // per CTA
 
-constexpr int MAX_MAPS = 24;
+constexpr int MAX_MAPS = 36;
 constexpr int MAX_PHASES = 24;
 constexpr int TILE_PARTS = 2 * EPI_WARPS;              // epilogue warps that finish one tile
 enum Epilogue : int32_t {

@@ -441,13 +441,18 @@ constexpr float NS_SCALE = 64.0f;
 constexpr int STEPS_PER_LAUNCH = 5;
 // Largest side (its band counters fit a launch) and largest stack.
 constexpr int64_t MUON_MAX_DIM = int64_t(1) << 18, MUON_MAX_BATCH = 65535;
-static_assert(3 * STEPS_PER_LAUNCH <= phases::MAX_PHASES, "phase table");
+static_assert(3 * STEPS_PER_LAUNCH + 2 <= phases::MAX_PHASES, "phase table");
 
 struct MuonSpace {
     int64_t side, ldx, lds;    // smaller side; row strides of X and of A, B
     int64_t per_launch;        // batch entries per launch
-    size_t x0, x1, a, b, part, norm, total;
+    int mats;                  // side x side matrices kept
+    size_t x0, x1, mat, mat_bytes, part, norm, total;
 };
+
+// Whether two steps may be taken at once (below).  Its precision was compared
+// with single steps' in fp16 for sides up to half the length: the same.
+bool muon_may_pair(int64_t m, int64_t n) { return std::max(m, n) >= 2 * std::min(m, n); }
 
 MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
 {
@@ -455,11 +460,12 @@ MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
     q.side = std::min(m, n);
     q.ldx = pad_to(n, 64);
     q.lds = pad_to(q.side, 8);
-    // counters of a launch: per step and entry the bands of A, of B and of X;
-    // beside them the arrivals of split products (fewer tiles than CTA pairs,
-    // so under 10,000 words)
+    q.mats = muon_may_pair(m, n) ? 6 : 2;
+    // counters of a launch: the bands of each phase's result; beside them the
+    // arrivals of split products (fewer tiles than CTA pairs, so under 10,000
+    // words)
     const int64_t nb = div_up(q.side, BM), mb = div_up(m, BM);
-    const int64_t words = STEPS_PER_LAUNCH * (2 * (1 + nb) + 1 + mb);
+    const int64_t words = 14 * (1 + nb) + STEPS_PER_LAUNCH * (1 + mb);
     q.per_launch = std::max<int64_t>(1, std::min<int64_t>(batch, 50000 / words));
     size_t o = 0;
     auto take = [&](int64_t bytes) {
@@ -469,8 +475,8 @@ MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
     };
     q.x0 = take(batch * m * q.ldx * 2);
     q.x1 = take(batch * m * q.ldx * 2);
-    q.a = take(q.per_launch * q.side * q.lds * 2);
-    q.b = take(q.per_launch * q.side * q.lds * 2);
+    q.mat_bytes = static_cast<size_t>(pad_to(q.per_launch * q.side * q.lds * 2, 256));
+    q.mat = take(q.mats * static_cast<int64_t>(q.mat_bytes));
     q.part = take(static_cast<int64_t>(2 * partial_bytes(sms)));
     q.norm = take(batch * muon_norm_blocks(m * n, sms) * 8);
     q.total = o;
@@ -479,6 +485,14 @@ MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
 
 // Steps [0, steps) of entries [first, first + count) from X0; the last one
 // stores bf16 into `out`.  X alternates between the two buffers.
+//
+// One step: A = X X^T, P = a I + b A + c A A, X <- P X.  Two steps at once:
+// P0 from A0 as above, then A1 = X1 X1^T = P0 A0 P0 without forming X1 (P0 is
+// a polynomial of A0, so everything commutes and every product is symmetric),
+// P1 from A1, and X2 = (P1 P0) X: three more products of the small side for
+// one X X^T and one P X less.  Of five steps the first two and the last two are
+// taken together when that is shorter: fp16's roundings act on P0's and A1's
+// entries where the step's map is steepest only in the middle ones.
 int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, int64_t first, int64_t count, int steps,
                 int& cur, bool last, const Mat& out, int pairs, cudaStream_t s)
 {
@@ -496,17 +510,21 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
     for (int i = 0; i < 2; ++i) {
         x[i] = Mat{ws.data + (i ? q.x1 : q.x0) + first * x_bytes, m, q.ldx, q.ldx, count, m * q.ldx, true};
     }
-    const Mat A{ws.data + q.a, side, side, q.lds, count, side * q.lds, true};
-    const Mat B{ws.data + q.b, side, side, q.lds, count, side * q.lds, true};
     const int64_t sb = div_up(side, BM);
     const int64_t gram_k = tall ? m : n;
-    auto cost = [&](int64_t tn) {
+    auto gram_us = [&](int64_t tn) {
         const int64_t tri = sb * (sb + 1) / 2 * (BM / tn) * count, nk = div_up(gram_k, BK);
-        return phase_us(tri, nk, split_parts(tri, nk, pairs, tn), pairs, tn) +
-               phase_us(tri, div_up(side, BK), 1, pairs, tn) +
-               phase_us(div_up(m, BM) * div_up(q.ldx, tn) * count, div_up(side, BK), 1, pairs, tn);
+        return phase_us(tri, nk, split_parts(tri, nk, pairs, tn), pairs, tn);
     };
-    const int64_t tn = cost(128) < cost(256) ? 128 : 256;
+    auto small_us = [&](int64_t tn) {
+        return phase_us(sb * (sb + 1) / 2 * (BM / tn) * count, div_up(side, BK), 1, pairs, tn);
+    };
+    auto update_us = [&](int64_t tn) {
+        return phase_us(div_up(m, BM) * div_up(q.ldx, tn) * count, div_up(side, BK), 1, pairs, tn);
+    };
+    auto step_us = [&](int64_t tn) { return gram_us(tn) + small_us(tn) + update_us(tn); };
+    const int64_t tn = step_us(128) < step_us(256) ? 128 : 256;
+    const bool pair = q.mats == 6 && steps == STEPS_PER_LAUNCH && 3 * small_us(tn) < gram_us(tn) + update_us(tn);
     p.tile_cols = static_cast<int32_t>(tn);
     // X as A and as B operand: K-major in one product, MN-major in the other
     int xa[2], xb[2], xc[2], xo[2];   // gram's A and B operands, the update's X operand, output
@@ -516,89 +534,127 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
         xc[i] = tall ? mp.k_major(x[i], A_ROWS) : mp.mn_major(x[i], tn / 2);
         xo[i] = mp.out(x[i]);
     }
-    const int aa = mp.k_major(A, A_ROWS), ab = mp.k_major(A, tn / 2), ao = mp.out(A), at = mp.out_t(A);
-    const int bk = mp.k_major(B, tall ? tn / 2 : A_ROWS), bo = mp.out(B), bt = mp.out_t(B);
+    // the symmetric matrices: as A and as B operand, stored and mirrored
+    struct Sym {
+        Mat m;
+        int8_t a, b, out, out_t;
+    };
+    Sym sym[6];
+    for (int i = 0; i < (pair ? 6 : 2); ++i) {
+        const Mat w{ws.data + q.mat + i * q.mat_bytes, side, side, q.lds, count, side * q.lds, true};
+        sym[i] = Sym{w, static_cast<int8_t>(mp.k_major(w, A_ROWS)), static_cast<int8_t>(mp.k_major(w, tn / 2)),
+                     static_cast<int8_t>(mp.out(w)), static_cast<int8_t>(mp.out_t(w))};
+    }
+    const Sym &A0 = sym[0], &P0 = sym[1], &AP = sym[2], &A1 = sym[3], &P1 = sym[4], &PP = sym[5];
     const int oo = last ? mp.out(out) : 0;
     if (mp.failed)
         return TFFN_ERR_INVALID_ARG;
     float* partial = reinterpret_cast<float*>(ws.data + q.part);
     int64_t most = 1;   // tasks of the largest phase
 
+    // A symmetric result's phase.
+    auto sym_phase = [&](const Sym& to, int64_t k) {
+        Phase f = make_phase(side, side, tn, k, 0, k);
+        f.batches = static_cast<int32_t>(count);
+        f.sym = 1;
+        f.n_tiles = static_cast<int32_t>(sb * (BM / tn));
+        f.f16 = f.out_f16 = 1;
+        f.out[0] = to.out;
+        f.out_t = to.out_t;
+        return f;
+    };
+    auto on_band = [&](const Phase& f) {
+        return depend(phases::DEP_BAND, f, f.n_tiles,
+                      f.sym ? phase_tiles(f, tn) / count : int64_t(f.m_tiles) * f.n_tiles);
+    };
+    auto on_all = [&](const Phase& f) {
+        Dep d = on_band(f);
+        d.mode = phases::DEP_ALL;
+        return d;
+    };
+    auto add = [&](Phase& f, int64_t bands, int parts) {
+        t.count_done(f, bands);
+        t.split(f, parts, partial);
+        t.add(f);
+        most = std::max(most, phase_tiles(f, tn) * f.splits);
+    };
+    // a I + b A + c A A of an A that `made` made
+    auto poly = [&](const Sym& a, const Sym& to, const Phase& made) {
+        Phase f = sym_phase(to, side);
+        f.map_a[0] = a.a;
+        f.map_b[0] = a.b;
+        f.alpha = NS_C;
+        f.beta = NS_B;
+        f.diag = NS_A;
+        f.aux0 = a.m.p;
+        f.aux_ld = q.lds;
+        f.aux_batch = a.m.bs;
+        f.dep_a = f.dep_b = on_band(made);
+        add(f, sb, 1);
+        return f;
+    };
+    // the product of two commuting symmetric matrices
+    auto product = [&](const Sym& a, const Phase& a_made, const Sym& b, const Phase& b_made, const Sym& to) {
+        Phase f = sym_phase(to, side);
+        f.map_a[0] = a.a;
+        f.map_b[0] = b.b;
+        f.dep_a = on_band(a_made);
+        f.dep_b = on_band(b_made);
+        add(f, sb, 1);
+        return f;
+    };
+
     Phase prev;   // the update that made the current X
     bool has_prev = false;
-    for (int i = 0; i < steps; ++i) {
+    for (int i = 0; i < steps;) {
+        const int group = pair && i != 2 ? 2 : 1;
         // A = X X^T (tall: X^T X) / 64^2
-        Phase gram = make_phase(side, side, tn, gram_k, 0, gram_k);
-        gram.batches = static_cast<int32_t>(count);
-        gram.sym = 1;
-        gram.n_tiles = static_cast<int32_t>(sb * (BM / tn));
-        gram.f16 = gram.out_f16 = 1;
+        Phase gram = sym_phase(A0, gram_k);
         gram.a_mn = gram.b_mn = gram.a4 = gram.b4 = tall ? 1 : 0;
         gram.map_a[0] = static_cast<int8_t>(xa[cur]);
         gram.map_b[0] = static_cast<int8_t>(xb[cur]);
         gram.alpha = 1.0f / (NS_SCALE * NS_SCALE);
-        gram.out[0] = static_cast<int8_t>(ao);
-        gram.out_t = static_cast<int8_t>(at);
-        if (has_prev) {
-            gram.dep_a = gram.dep_b = depend(tall ? phases::DEP_ALL : phases::DEP_BAND, prev, prev.n_tiles,
-                                             int64_t(prev.m_tiles) * prev.n_tiles);
+        if (has_prev)
+            gram.dep_a = gram.dep_b = tall ? on_all(prev) : on_band(prev);
+        add(gram, sb, split_parts(phase_tiles(gram, tn), gram.nk[0], pairs, tn));
+
+        Phase made = poly(A0, P0, gram);
+        const Sym* P = &P0;
+        if (group == 2) {
+            const Phase ap = product(A0, gram, P0, made, AP);
+            const Phase a1 = product(AP, ap, P0, made, A1);
+            const Phase p1 = poly(A1, P1, a1);
+            made = product(P1, p1, P0, made, PP);
+            P = &PP;
         }
-        t.count_done(gram, sb);
-        t.split(gram, split_parts(phase_tiles(gram, tn), gram.nk[0], pairs, tn), partial);
-        most = std::max(most, phase_tiles(gram, tn) * gram.splits);
-        t.add(gram);
 
-        // B = a I + b A + c A A
-        Phase sq = make_phase(side, side, tn, side, 0, side);
-        sq.batches = static_cast<int32_t>(count);
-        sq.sym = 1;
-        sq.n_tiles = gram.n_tiles;
-        sq.f16 = sq.out_f16 = 1;
-        sq.map_a[0] = static_cast<int8_t>(aa);
-        sq.map_b[0] = static_cast<int8_t>(ab);
-        sq.alpha = NS_C;
-        sq.beta = NS_B;
-        sq.diag = NS_A;
-        sq.aux0 = A.p;
-        sq.aux_ld = q.lds;
-        sq.aux_batch = A.bs;
-        sq.out[0] = static_cast<int8_t>(bo);
-        sq.out_t = static_cast<int8_t>(bt);
-        sq.dep_a = sq.dep_b = depend(phases::DEP_BAND, gram, gram.n_tiles, phase_tiles(gram, tn) / count);
-        t.count_done(sq, sb);
-        t.split(sq, 1, partial);
-        t.add(sq);
-
-        // X <- B X (tall: X B)
-        const bool end = last && i + 1 == steps;
+        // X <- P X (tall: X P)
+        i += group;
+        const bool end = last && i == steps;
         Phase up = make_phase(m, end ? n : q.ldx, tn, side, 0, side);
         up.batches = static_cast<int32_t>(count);
         up.f16 = 1;
         up.out_f16 = end ? 0 : 1;
         up.alpha = end ? 1.0f / NS_SCALE : 1.0f;
         up.out[0] = static_cast<int8_t>(end ? oo : xo[cur ^ 1]);
-        const Dep on_b = depend(phases::DEP_BAND, sq, sq.n_tiles, phase_tiles(sq, tn) / count);
+        const Dep on_p = on_band(made);
         Dep on_x;
         std::memset(&on_x, 0, sizeof(on_x));
         if (has_prev)
-            on_x = depend(tall ? phases::DEP_BAND : phases::DEP_ALL, prev, prev.n_tiles,
-                          int64_t(prev.m_tiles) * prev.n_tiles);
+            on_x = tall ? on_band(prev) : on_all(prev);
         if (tall) {
             up.map_a[0] = static_cast<int8_t>(xc[cur]);
-            up.map_b[0] = static_cast<int8_t>(bk);
+            up.map_b[0] = P->b;
             up.dep_a = on_x;
-            up.dep_b = on_b;
+            up.dep_b = on_p;
         } else {
-            up.map_a[0] = static_cast<int8_t>(bk);
+            up.map_a[0] = P->a;
             up.map_b[0] = static_cast<int8_t>(xc[cur]);
             up.b_mn = up.b4 = 1;
-            up.dep_a = on_b;
+            up.dep_a = on_p;
             up.dep_b = on_x;
         }
-        t.count_done(up, up.m_tiles);
-        t.split(up, 1, partial);
-        t.add(up);
-        most = std::max(most, phase_tiles(up, tn));
+        add(up, up.m_tiles, 1);
         prev = up;
         has_prev = true;
         cur ^= 1;
@@ -642,7 +698,9 @@ int muon_run(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int 
             if (direct)
                 dst = Mat{static_cast<uint8_t*>(out) + e * m * n * 2, m, n, n, count, m * n, false};
             else {
-                const int buf = (cur ^ (k & 1));   // the buffer that the last step would write
+                // the buffer that the launch's last update would write: five
+                // steps make five or three of them
+                const int buf = cur ^ (k & 1);
                 dst = Mat{ws.data + (buf ? q.x1 : q.x0) + e * m * q.ldx * 2, m, n, q.ldx, count, m * q.ldx, false};
                 end = buf;
             }
