@@ -70,10 +70,20 @@ def test_stacks(cuda_lib, batch, m, n):
 
 def test_large_stack(cuda_lib):
     """More entries than one launch's counters hold."""
-    G = _matrix(3000, 24, 40, seed=4)
-    out = _check(cuda_lib, G, tol=8e-3)     # the worst of 3000 small matrices
+    out = _check(cuda_lib, _matrix(3000, 72, 80, seed=4), tol=8e-3)     # the worst of 3000 small matrices
     assert cuda_lib.last_launch_count() > 3
     assert torch.isfinite(out).all()
+    _check(cuda_lib, _matrix(3000, 24, 40, seed=4))
+
+
+@pytest.mark.parametrize("m,n", [(31, 33), (32, 4000), (33, 33), (63, 65), (64, 14336), (5000, 64), (65, 65), (64, 1),
+                                 (33, 1000)])
+@pytest.mark.parametrize("steps", [1, 5, 8])
+def test_small_sides(cuda_lib, m, n, steps):
+    """A side of at most 64 is iterated in fp32: only the result's rounding to
+    bf16 (1.7e-3 of its norm) is left; 2.2e-3 is allowed.  (65 is not small.)"""
+    _check(cuda_lib, _matrix(m, n, seed=m + n), steps=steps, tol=2.2e-3 if min(m, n) <= 64 else 5e-3)
+    _check(cuda_lib, _matrix(3, m, n, seed=m + n, dtype=BF), steps=steps, tol=2.2e-3 if min(m, n) <= 64 else 5e-3)
 
 
 @pytest.mark.parametrize("steps", [1, 2, 5, 6, 10, 11])

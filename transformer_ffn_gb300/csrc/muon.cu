@@ -1,6 +1,7 @@
-// muon.cu -- the memory-bound ends of muon_orthogonalize: the Frobenius norm,
-// the scaled fp16 copy that the Newton-Schulz products start from, and the
-// dense copy of a result whose rows the products stored padded.
+// muon.cu -- muon_orthogonalize beside its large products: the Frobenius norm,
+// the scaled fp16 copy that the Newton-Schulz products start from, the dense
+// copy of a result whose rows the products stored padded, and the whole
+// iteration for matrices with a small side.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -95,19 +96,16 @@ __global__ void __launch_bounds__(THREADS) muon_norm_kernel(const T* G, int64_t 
     }
 }
 
-// X[r][c] = fp16(scale G[r][c] / (norm + eps)), zero in the padding columns.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t m, int64_t n, const double* part,
-                                                            int blocks, float scale, float eps, __half* X, int64_t ld,
-                                                            int vec)
+// One entry's factor from its blocks' sums: X = (G before) factor = scale G /
+// (norm + eps).  A norm past 2^60 is first brought down, so that neither number
+// leaves fp32's normal range.  Called by a whole block.
+__device__ __forceinline__ float2 entry_factor(const double* part, int blocks, float scale, float eps)
 {
     __shared__ double red[THREADS / 32];
-    __shared__ float factor, before;
-    const T* g = G + blockIdx.y * m * n;
-    __half* x = X + blockIdx.y * m * ld;
+    __shared__ float2 result;
     double d = 0.0;
     for (int k = threadIdx.x; k < blocks; k += THREADS)
-        d += part[static_cast<int64_t>(blockIdx.y) * blocks + k];
+        d += part[k];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         d += __shfl_xor_sync(0xffffffffu, d, o);
@@ -118,15 +116,25 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
         d = 0.0;
         for (int k = 0; k < THREADS / 32; ++k)
             d += red[k];
-        // X = (G before) factor: a norm past 2^60 is first brought down, so that
-        // neither number leaves fp32's normal range
         const double norm = sqrt(d) + static_cast<double>(eps);
         const double pre = norm > 0x1p60 ? 0x1p-60 : 1.0;
-        before = static_cast<float>(pre);
-        factor = static_cast<float>(static_cast<double>(scale) / (norm * pre));
+        result = make_float2(static_cast<float>(pre),
+                             static_cast<float>(static_cast<double>(scale) / (norm * pre)));
     }
     __syncthreads();
-    const float f = factor, f0 = before;
+    return result;
+}
+
+// X[r][c] = fp16(scale G[r][c] / (norm + eps)), zero in the padding columns.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t m, int64_t n, const double* part,
+                                                            int blocks, float scale, float eps, __half* X, int64_t ld,
+                                                            int vec)
+{
+    const T* g = G + blockIdx.y * m * n;
+    __half* x = X + blockIdx.y * m * ld;
+    const float2 fs = entry_factor(part + static_cast<int64_t>(blockIdx.y) * blocks, blocks, scale, eps);
+    const float f0 = fs.x, f = fs.y;
     const int64_t per_row = ld / 8;
     const int64_t total = m * per_row;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < total;
@@ -154,6 +162,228 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
             o[j] = __floats2half2_rn(v[2 * j] * f0 * f, v[2 * j + 1] * f0 * f);
         *reinterpret_cast<uint4*>(x + r * ld + c) = *reinterpret_cast<const uint4*>(o);
     }
+}
+
+// ---- small sides.  With at most 64 rows (or columns) the iteration runs on the
+// side x side matrix A = X X^T alone, in fp32: X_k = Q_k X_0 with Q_{k+1} = P_k
+// Q_k, P_k = a I + b A_k + c A_k^2 and A_{k+1} = P_k A_k P_k (polynomials of A_0
+// commute, so all of these are symmetric).  Two kernels beside the norm: A_0 in
+// parts of the long side, and Q with its product.  Every block of the second
+// runs the whole iteration (18 products of side^3, each about 3 us at 64 and
+// bound by shared-memory loads and their latency) before its share of the
+// product, which costs nothing beside handing Q over.  Measured: 16 x 300 22 us,
+// 64 x 4096 72 us, where fifteen dependent phases of tensor-core products take
+// 75 us and more; and fp32 keeps what fp16 loses where few entries make a
+// matrix (3e-3 of its norm with 16 rows).
+constexpr int CHUNK = 64;   // long-side elements in shared memory at a time
+
+// One chunk of an entry, [S short][CHUNK long], scaled; zero outside.
+template <typename T, int S>
+__device__ __forceinline__ void load_chunk(const T* g, bool tall, int side, int64_t len, int64_t c0, float2 fs,
+                                           float (*x)[CHUNK + 4])
+{
+    for (int i = threadIdx.x; i < S * CHUNK; i += THREADS) {
+        // neighbouring threads read neighbouring elements either way
+        const int k = tall ? i % S : i / CHUNK, c = tall ? i / S : i % CHUNK;
+        float v = 0.0f;
+        if (k < side && c0 + c < len)
+            v = to_f(g[tall ? (c0 + c) * side + k : k * len + c0 + c]);
+        x[k][c] = v * fs.x * fs.y;
+    }
+}
+
+// A thread's MT x MT block of the S x S result, rows i0.., columns j0..
+template <int S>
+struct Tile {
+    static constexpr int MT = S / 16;   // 16 x 16 threads
+    int i0, j0;
+    __device__ __forceinline__ Tile() : i0((threadIdx.x / 16) * MT), j0((threadIdx.x % 16) * MT) {}
+};
+
+// part[entry][chunk set][S][S]: partial sums of X X^T.
+template <typename T, int S>
+__global__ void __launch_bounds__(THREADS) muon_small_gram_kernel(const T* G, bool tall, int side, int64_t len,
+                                                                  const double* norm, int blocks, float eps,
+                                                                  float* part)
+{
+    __shared__ float x[S][CHUNK + 4];
+    constexpr int MT = Tile<S>::MT;
+    const Tile<S> t;
+    const T* g = G + blockIdx.y * (static_cast<int64_t>(side) * len);
+    const float2 fs = entry_factor(norm + static_cast<int64_t>(blockIdx.y) * blocks, blocks, 1.0f, eps);
+    float acc[MT][MT] = {};
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * CHUNK; c0 < len;
+         c0 += static_cast<int64_t>(gridDim.x) * CHUNK) {
+        __syncthreads();
+        load_chunk<T, S>(g, tall, side, len, c0, fs, x);
+        __syncthreads();
+        for (int c = 0; c < CHUNK; c += 4) {
+            float4 a[MT], b[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                a[i] = *reinterpret_cast<const float4*>(&x[t.i0 + i][c]);
+                b[i] = *reinterpret_cast<const float4*>(&x[t.j0 + i][c]);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    acc[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+        }
+    }
+    float* out = part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * S * S;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            out[(t.i0 + i) * S + t.j0 + j] = acc[i][j];
+}
+
+template <int S>
+using Square = float[S][S + 4];   // rows stay on 16-byte boundaries
+
+// MT consecutive values of a row, from a multiple of MT.
+template <int MT>
+__device__ __forceinline__ void load_run(const float* p, float (&v)[MT])
+{
+    static_assert(MT == 2 || MT == 4, "one shared-memory load");
+    if constexpr (MT == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x;
+        v[1] = x.y;
+    }
+}
+
+// out = alpha A B + beta C + diag I of symmetric matrices (C nullable).
+template <int S>
+__device__ __forceinline__ void product(const Square<S>& A, const Square<S>& B, Square<S>& out, float alpha,
+                                        float beta, const Square<S>* C, float diag)
+{
+    constexpr int MT = Tile<S>::MT;
+    const Tile<S> t;
+    float acc[MT][MT] = {};
+#pragma unroll 8
+    for (int k = 0; k < S; ++k) {
+        float a[MT], b[MT];
+        load_run(&A[k][t.i0], a);   // row k for column k: A is symmetric
+        load_run(&B[k][t.j0], b);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int r = t.i0 + i, c = t.j0 + j;
+            float v = alpha * acc[i][j] + (r == c ? diag : 0.0f);
+            if (C != nullptr)
+                v = fmaf(beta, (*C)[r][c], v);
+            out[r][c] = v;
+        }
+    __syncthreads();
+}
+
+template <int S>
+struct SmallShared {
+    Square<S> a, p, t, q[2];
+    float x[S][CHUNK + 4];
+};
+
+template <typename T, int S>
+__global__ void __launch_bounds__(THREADS) muon_small_apply_kernel(const T* G, bool tall, int side, int64_t len,
+                                                                   const double* norm, int blocks, float eps,
+                                                                   const float* part, int parts, int steps, float ca,
+                                                                   float cb, float cc, __nv_bfloat16* out)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    SmallShared<S>& sh = *reinterpret_cast<SmallShared<S>*>(smem);
+    constexpr int MT = Tile<S>::MT;
+    const Tile<S> t;
+    const int64_t entry = static_cast<int64_t>(blockIdx.y) * side * len;
+    const float2 fs = entry_factor(norm + static_cast<int64_t>(blockIdx.y) * blocks, blocks, 1.0f, eps);
+    const float* src = part + static_cast<int64_t>(blockIdx.y) * parts * S * S;
+    for (int i = threadIdx.x; i < S * S; i += THREADS) {
+        float v = 0.0f;
+        for (int k = 0; k < parts; ++k)
+            v += __ldg(src + static_cast<int64_t>(k) * S * S + i);
+        sh.a[i / S][i % S] = v;
+        sh.q[0][i / S][i % S] = i / S == i % S ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    int cur = 0;
+    for (int k = 0; k < steps; ++k) {
+        product<S>(sh.a, sh.a, sh.p, cc, cb, &sh.a, ca);
+        product<S>(sh.p, sh.q[cur], sh.q[cur ^ 1], 1.0f, 0.0f, nullptr, 0.0f);
+        cur ^= 1;
+        if (k + 1 < steps) {
+            product<S>(sh.a, sh.p, sh.t, 1.0f, 0.0f, nullptr, 0.0f);
+            product<S>(sh.t, sh.p, sh.a, 1.0f, 0.0f, nullptr, 0.0f);
+        }
+    }
+    const Square<S>& Q = sh.q[cur];
+    constexpr int CT = CHUNK / 16;   // long-side elements of a thread
+    const int c_first = (threadIdx.x % 16) * CT;
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * CHUNK; c0 < len;
+         c0 += static_cast<int64_t>(gridDim.x) * CHUNK) {
+        __syncthreads();
+        load_chunk<T, S>(G + entry, tall, side, len, c0, fs, sh.x);
+        __syncthreads();
+        float acc[MT][CT] = {};
+#pragma unroll 4
+        for (int k = 0; k < S; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(&sh.x[k][c_first]);
+            float q[MT];
+            load_run(&Q[k][t.i0], q);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                acc[i][0] = fmaf(q[i], x.x, acc[i][0]);
+                acc[i][1] = fmaf(q[i], x.y, acc[i][1]);
+                acc[i][2] = fmaf(q[i], x.z, acc[i][2]);
+                acc[i][3] = fmaf(q[i], x.w, acc[i][3]);
+            }
+        }
+        // through shared memory, so that neighbouring threads store neighbours
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            *reinterpret_cast<float4*>(&sh.x[t.i0 + i][c_first]) =
+                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        __syncthreads();
+        for (int i = threadIdx.x; i < S * CHUNK; i += THREADS) {
+            const int k = tall ? i % S : i / CHUNK, c = tall ? i / S : i % CHUNK;
+            if (k < side && c0 + c < len)
+                out[entry + (tall ? (c0 + c) * side + k : k * len + c0 + c)] = __float2bfloat16_rn(sh.x[k][c]);
+        }
+    }
+}
+
+template <typename T, int S>
+int small(const T* G, int64_t batch, bool tall, int side, int64_t len, const double* norm, int blocks, float eps,
+          float* part, int parts, int steps, const float* abc, __nv_bfloat16* out, int sms, cudaStream_t s)
+{
+    static bool ready = false;
+    if (!ready && cudaFuncSetAttribute(muon_small_apply_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       sizeof(SmallShared<S>)) != cudaSuccess)
+        return -1;
+    ready = true;
+    const int64_t chunks = (len + CHUNK - 1) / CHUNK;
+    const unsigned y = static_cast<unsigned>(batch);
+    muon_small_gram_kernel<T, S>
+        <<<dim3(static_cast<unsigned>(parts), y), THREADS, 0, s>>>(G, tall, side, len, norm, blocks, eps, part);
+    // one block an SM: each runs the whole iteration
+    const int64_t x = std::max<int64_t>(1, std::min<int64_t>(chunks, int64_t(sms) / batch));
+    muon_small_apply_kernel<T, S><<<dim3(static_cast<unsigned>(x), y), THREADS, sizeof(SmallShared<S>), s>>>(
+        G, tall, side, len, norm, blocks, eps, part, parts, steps, abc[0], abc[1], abc[2], out);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 // 16-bit rows of stride ld to dense rows of n.
@@ -188,6 +418,43 @@ int muon_norm_blocks(int64_t elems, int sms)
     // eight values a thread at least, at most four blocks an SM
     return static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * 4, elems / (muon::THREADS * 8))));
+}
+
+int muon_small_side() { return 64; }
+
+// Parts of the long side: enough to occupy the GPU, at most 32 (every block of
+// the second kernel adds them all).
+int muon_small_parts(int64_t batch, int64_t len, int sms)
+{
+    const int64_t chunks = (len + muon::CHUNK - 1) / muon::CHUNK;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(chunks, 32), 2 * int64_t(sms) / batch)));
+}
+
+size_t muon_small_bytes(int64_t batch, int64_t side, int64_t len, int sms)
+{
+    const int64_t S = side <= 32 ? 32 : 64;
+    return static_cast<size_t>(batch * muon_small_parts(batch, len, sms) * S * S * 4);
+}
+
+int launch_muon_small(const void* G, bool f32, int64_t batch, int64_t m, int64_t n, const double* norm, int blocks,
+                      float eps, float* part, int steps, const float* abc, void* out, int sms, cudaStream_t s)
+{
+    const bool tall = m > n;
+    const int side = static_cast<int>(std::min(m, n));
+    const int64_t len = std::max(m, n);
+    const int parts = muon_small_parts(batch, len, sms);
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    const float* gf = static_cast<const float*>(G);
+    const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(G);
+    if (side <= 32)
+        return f32 ? muon::small<float, 32>(gf, batch, tall, side, len, norm, blocks, eps, part, parts, steps, abc, o,
+                                            sms, s)
+                   : muon::small<__nv_bfloat16, 32>(gb, batch, tall, side, len, norm, blocks, eps, part, parts, steps,
+                                                    abc, o, sms, s);
+    return f32 ? muon::small<float, 64>(gf, batch, tall, side, len, norm, blocks, eps, part, parts, steps, abc, o, sms,
+                                        s)
+               : muon::small<__nv_bfloat16, 64>(gb, batch, tall, side, len, norm, blocks, eps, part, parts, steps, abc,
+                                                o, sms, s);
 }
 
 int launch_muon_norm(const void* G, bool f32, int64_t batch, int64_t elems, double* part, int blocks, cudaStream_t s)

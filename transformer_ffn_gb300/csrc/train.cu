@@ -457,6 +457,7 @@ bool muon_may_pair(int64_t m, int64_t n) { return std::max(m, n) >= 2 * std::min
 MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
 {
     MuonSpace q;
+    std::memset(&q, 0, sizeof(q));
     q.side = std::min(m, n);
     q.ldx = pad_to(n, 64);
     q.lds = pad_to(q.side, 8);
@@ -473,12 +474,17 @@ MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
         o += static_cast<size_t>(pad_to(bytes, 256));
         return at;
     };
+    q.norm = take(batch * muon_norm_blocks(m * n, sms) * 8);
+    if (q.side <= muon_small_side()) {
+        q.part = take(static_cast<int64_t>(muon_small_bytes(batch, q.side, std::max(m, n), sms)));
+        q.total = o;
+        return q;
+    }
     q.x0 = take(batch * m * q.ldx * 2);
     q.x1 = take(batch * m * q.ldx * 2);
     q.mat_bytes = static_cast<size_t>(pad_to(q.per_launch * q.side * q.lds * 2, 256));
     q.mat = take(q.mats * static_cast<int64_t>(q.mat_bytes));
     q.part = take(static_cast<int64_t>(2 * partial_bytes(sms)));
-    q.norm = take(batch * muon_norm_blocks(m * n, sms) * 8);
     q.total = o;
     return q;
 }
@@ -681,9 +687,20 @@ int muon_run(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int 
     const bool f32 = dtype == TFFN_F32;
     double* part = reinterpret_cast<double*>(ws.data + q.norm);
     const int blocks = muon_norm_blocks(m * n, sms);
+    if (launch_muon_norm(G, f32, batch, m * n, part, blocks, s) != 0)
+        return TFFN_ERR_CUDA;
+    if (q.side <= muon_small_side()) {
+        const float abc[3] = {NS_A, NS_B, NS_C};
+        api_timing_start(s);
+        if (launch_muon_small(G, f32, batch, m, n, part, blocks, NS_EPS, reinterpret_cast<float*>(ws.data + q.part),
+                              steps, abc, out, sms, s) != 0)
+            return TFFN_ERR_CUDA;
+        api_timing_stop(s);
+        api_launches(3);
+        return TFFN_OK;
+    }
     int launches = 2;
-    if (launch_muon_norm(G, f32, batch, m * n, part, blocks, s) != 0 ||
-        launch_muon_pack(G, f32, batch, m, n, part, blocks, NS_SCALE, NS_EPS, ws.data + q.x0, q.ldx, sms, s) != 0)
+    if (launch_muon_pack(G, f32, batch, m, n, part, blocks, NS_SCALE, NS_EPS, ws.data + q.x0, q.ldx, sms, s) != 0)
         return TFFN_ERR_CUDA;
     // rows of the result that TMA can store where they belong, else through X's buffer
     const bool direct = n % 8 == 0 && aligned(out, 16);
