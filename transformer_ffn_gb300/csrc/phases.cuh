@@ -19,7 +19,7 @@
 // smaller tickets, so the launch finishes with any number of resident CTAs.
 //
 // The main loop is the FFN engine's (engine.cuh): clusters of two CTAs, a ring
-// of 192 KiB of stages per CTA, an A and a B loader and one MMA thread; a
+// of five 32 KiB stages per CTA (the sixth stage's room serves the epilogue), an A and a B loader and one MMA thread; a
 // scheduler thread claims the tickets.  The epilogue has eight warps, two per tensor
 // memory lane quadrant and so two per scheduler, each taking half of the
 // tile's columns, 32 at a time, through two 2 KiB staging buffers: a tile's
@@ -52,12 +52,13 @@ constexpr int NUM_THREADS = 32 * (4 + EPI_WARPS);
 constexpr uint32_t TASK_CONSUMERS = 2 * (2 + EPI_WARPS) + 1;
 constexpr int OUT_BUF_BYTES = 32 * 32 * 2;                 // 32 rows x 32 columns
 constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;   // 32 KiB
+constexpr int IN_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;    // as much for the epilogue's own operands
 
 template <int TN>
 struct Geo {
     static constexpr int STAGE_BYTES = A_STAGE_BYTES + TN / 2 * BK * 2;
-    static constexpr int STAGES = TN == 256 ? 6 : 8;       // 192 KiB either way
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + AUX_BYTES + 1024;
+    static constexpr int STAGES = TN == 256 ? 5 : 6;       // 160 or 144 KiB
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + IN_BYTES + AUX_BYTES + 1024;
     static constexpr int PART_VEC = BM * TN / 4;           // float4 of one K part of a tile
     static constexpr int PART_WARP_VEC = PART_VEC / TILE_PARTS;
 };
@@ -511,6 +512,7 @@ struct TileCtx {
     int32_t batch;
     int lane;
     uint32_t stage;      // the warp's two staging buffers
+    uint32_t in;         // its two buffers for operands
 };
 
 // The staged box to global memory.
@@ -563,6 +565,51 @@ __device__ __forceinline__ void put_box_t(const CUtensorMap* map, const TileCtx&
     sb ^= 1u;
 }
 
+// A chunk (32 rows x 32 columns of 2 bytes, from column x) of a 16-bit tensor
+// into one of the warp's operand buffers, four lanes to a row, laid out like a
+// staged box; zeros outside the matrix.  Each lane reading its own row straight
+// from memory asked for half a sector of 32 rows at a time: 18 us for the G and
+// U of a 256 x 256 tile.  Past L1: C may have been written in this launch.
+__device__ __forceinline__ void fetch_chunk(uint32_t buf, const void* base, int64_t ld, int32_t rows, int32_t ncols,
+                                            const TileCtx& t, int32_t x)
+{
+    const int32_t piece = t.lane & 3, c = x + piece * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t r = (t.lane >> 2) + i * 8, row = t.row0 + r;
+        const bool in = row < rows && c < ncols;
+        const uint16_t* src = static_cast<const uint16_t*>(base) + (in ? row * ld + c : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         buf + static_cast<uint32_t>(r * 64 + ((piece ^ ((r >> 1) & 3)) << 4))),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
+
+__device__ __forceinline__ void fetch_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The chunks fetched before are in shared memory, for every lane.
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+}
+
+// This lane's row of a fetched chunk.
+__device__ __forceinline__ void read_row(uint32_t buf, int lane, uint4 (&v)[4])
+{
+    const uint32_t at = buf + static_cast<uint32_t>(lane) * 64u, sw = static_cast<uint32_t>(lane >> 1) & 3u;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                     : "r"(at + ((j ^ sw) << 4))
+                     : "memory");
+}
+
 // out = alpha D + beta C + diag I (AUX: with the last two).
 template <bool AUX>
 __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
@@ -570,24 +617,13 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
 {
     const float alpha = f.alpha, beta = f.beta, diag = f.diag;
     const bool f16 = f.out_f16 != 0;
-    const int32_t row = t.row0 + t.lane;
-    const int32_t ncols = f.ncols;
-    const __half* c_row = nullptr;
-    if (AUX && row < f.rows)
-        c_row = static_cast<const __half*>(f.aux0) + t.batch * f.aux_batch + static_cast<int64_t>(row) * f.aux_ld;
     const CUtensorMap* map = &p.map[f.out[0]];
     const CUtensorMap* map_t = &p.map[f.out_t];
-    // C's rows are 16-byte aligned and padded to 8 columns.  They may have been
-    // written earlier in this launch: read past L1, one chunk ahead.
-    uint4 cv[4];
+    // C's rows are 16-byte aligned and padded to 8 columns; read one chunk ahead
+    const __half* c_base = static_cast<const __half*>(f.aux0) + t.batch * f.aux_batch;
     auto load_c = [&](int c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int32_t x = t.col0 + c * 32 + 8 * j;
-            cv[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (c_row != nullptr && x < ncols)
-                cv[j] = __ldcg(reinterpret_cast<const uint4*>(c_row + x));
-        }
+        fetch_chunk(t.in, c_base, f.aux_ld, f.rows, f.ncols, t, t.col0 + c * 32);
+        fetch_commit();
     };
     if (AUX)
         load_c(0);
@@ -598,6 +634,12 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
         float v[32];
         source32(src, t.tcol + c * 32, c, v);
         if (AUX) {
+            uint4 cv[4];
+            fetch_wait();
+            read_row(t.in, t.lane, cv);
+            __syncwarp();
+            if (c + 1 < t.nchunks)
+                load_c(c + 1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t cw[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
@@ -608,8 +650,6 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
                     v[j * 8 + q * 2 + 1] = fmaf(alpha, v[j * 8 + q * 2 + 1], beta * cf.y);
                 }
             }
-            if (c + 1 < t.nchunks)
-                load_c(c + 1);
             if (x == t.row0) {   // this box is on the diagonal: column = lane
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -659,6 +699,14 @@ __device__ __forceinline__ uint32_t epi_glu_save(const Params& p, const Phase& f
     return sb;
 }
 
+__device__ __forceinline__ void fetch_gu(const Phase& f, const TileCtx& t, int c)
+{
+    const int32_t x = t.col0 + c * 32;
+    fetch_chunk(t.in, f.aux0, f.aux_ld, f.rows, f.ncols, t, x);
+    fetch_chunk(t.in + OUT_BUF_BYTES, f.aux1, f.aux_ld, f.rows, f.ncols, t, x);
+    fetch_commit();
+}
+
 // D = dH: dU = dH act(G), dG = dH U act'(G), and H = act(G) U again for dW2
 // (recomputed rather than kept: the forward pass would have to write it and
 // the caller to hold it, for the same read here).
@@ -666,29 +714,18 @@ template <int ACT>
 __device__ __forceinline__ uint32_t epi_glu_grad(const Params& p, const Phase& f, const Source& src,
                                                  const TileCtx& t, uint32_t sb)
 {
-    const int32_t row = t.row0 + t.lane;
-    const __nv_bfloat16 *g_row = nullptr, *u_row = nullptr;
-    if (row < f.rows) {
-        g_row = static_cast<const __nv_bfloat16*>(f.aux0) + static_cast<int64_t>(row) * f.aux_ld;
-        u_row = static_cast<const __nv_bfloat16*>(f.aux1) + static_cast<int64_t>(row) * f.aux_ld;
-    }
-    const int32_t ncols = f.ncols;
-    uint4 gv[4], uv[4];   // 32 columns of G and U, read one chunk ahead
-    auto load_gu = [&](int c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int32_t x = t.col0 + c * 32 + 8 * j;
-            gv[j] = uv[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (g_row != nullptr && x < ncols) {
-                gv[j] = __ldg(reinterpret_cast<const uint4*>(g_row + x));
-                uv[j] = __ldg(reinterpret_cast<const uint4*>(u_row + x));
-            }
-        }
-    };
-    load_gu(0);
 #pragma unroll 1
     for (int c = 0; c < t.nchunks; ++c) {
         const int32_t x = t.col0 + c * 32;
+        // G and U of this chunk were fetched a chunk ahead (the first one before
+        // the accumulator was waited for)
+        uint4 gv[4], uv[4];
+        fetch_wait();
+        read_row(t.in, t.lane, gv);
+        read_row(t.in + OUT_BUF_BYTES, t.lane, uv);
+        __syncwarp();
+        if (c + 1 < t.nchunks)
+            fetch_gu(f, t, c + 1);
         float d[32];
         source32(src, t.tcol + c * 32, c, d);
         uint32_t dg[16], du[16], hh[16];
@@ -709,8 +746,6 @@ __device__ __forceinline__ uint32_t epi_glu_grad(const Params& p, const Phase& f
                 hh[i] = pack_bf16x2(a0 * u0, a1 * u1);
             }
         }
-        if (c + 1 < t.nchunks)
-            load_gu(c + 1);
         put_box(&p.map[f.out[0]], t, sb, dg, x);
         put_box(&p.map[f.out[1]], t, sb, du, x);
         put_box(&p.map[f.out[2]], t, sb, hh, x);
@@ -743,7 +778,7 @@ __device__ __forceinline__ uint32_t epilogue_tile(const Params& p, const Phase& 
 
 template <int TN>
 __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank,
-                             int warp, int lane, uint32_t out_stage)
+                             int warp, int lane, uint32_t out_stage, uint32_t in_stage)
 {
     using G = Geo<TN>;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);         // TMEM lanes [32 quad, 32 quad + 32)
@@ -757,9 +792,6 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
             break;
         const Phase& f = p.ph[task.x];
         const uint32_t acc = iter & 1u;
-        if (!wait_mbar(w, ptx::smem_u32(&aux.tmem_full[acc]), (iter >> 1) & 1u, SITE_TMEM_FULL))
-            break;
-        ptx::tc_fence_after();
         TileCtx t;
         const int32_t cols = (f.epi == EPI_GLU_SAVE ? TN / 2 : TN) / 2;   // output columns of this warp
         t.row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA + static_cast<int32_t>(quad) * 32;
@@ -770,12 +802,18 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
         t.batch = task_batch(task);
         t.lane = lane;
         t.stage = out_stage;
+        t.in = in_stage;
         Source src;
         src.taddr = tmem_base + ((quad * 32u) << 16) + acc * TN;
         src.parts = nullptr;
         src.nparts = 0;
         src.part_vec = G::PART_VEC;
         const bool inside = t.row0 < f.rows && t.nchunks > 0;   // else this warp stores nothing
+        if (f.epi == EPI_GLU_GRAD && inside)
+            fetch_gu(f, t, 0);
+        if (!wait_mbar(w, ptx::smem_u32(&aux.tmem_full[acc]), (iter >> 1) & 1u, SITE_TMEM_FULL))
+            break;
+        ptx::tc_fence_after();
         bool finish = inside;
         if (f.splits > 1) {
             // This part's sums to memory; the last part of the tile to arrive
@@ -841,7 +879,8 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
             __syncwarp();
         }
     }
-    // Every store of this warp has completed before the CTA can leave.
+    // Every copy and store of this warp has completed before the CTA can leave.
+    fetch_wait();
     if (lane == 0) {
         ptx::bulk_wait_group<0>();
         __threadfence();
@@ -857,7 +896,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
     uint8_t* stages = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     constexpr int STAGES = Geo<TN>::STAGES, RING_BYTES = STAGES * Geo<TN>::STAGE_BYTES;
-    Aux<TN>& aux = *reinterpret_cast<Aux<TN>*>(stages + RING_BYTES + OUT_BYTES);
+    Aux<TN>& aux = *reinterpret_cast<Aux<TN>*>(stages + RING_BYTES + OUT_BYTES + IN_BYTES);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -905,7 +944,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
             run_scheduler<TN>(p, aux, w);
     } else {
         run_epilogue<TN>(p, aux, w, tmem_base, rank, warp, lane,
-                     ptx::smem_u32(stages + RING_BYTES) +
+                     ptx::smem_u32(stages + RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES),
+                     ptx::smem_u32(stages + RING_BYTES + OUT_BYTES) +
                          static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES));
     }
     __syncwarp();
