@@ -7,8 +7,8 @@
 
 namespace tffn {
 
-// Fills a launch of the TN-column kernel; the grid's cap is queried once.
-template <int TN>
+// Fills a launch of one form of the kernel; the grid's cap is queried once.
+template <int TN, bool IN>
 static int phase_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int* resident)
 {
     static int pairs = 0;
@@ -17,16 +17,16 @@ static int phase_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int*
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.blockDim = dim3(phases::NUM_THREADS);
-    cfg.dynamicSmemBytes = phases::Geo<TN>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = phases::Geo<TN, IN>::SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(2);
     if (pairs == 0) {
-        if (cudaFuncSetAttribute(phases::phase_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 phases::Geo<TN>::SMEM_BYTES) != cudaSuccess)
+        if (cudaFuncSetAttribute(phases::phase_kernel<TN, IN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 phases::Geo<TN, IN>::SMEM_BYTES) != cudaSuccess)
             return -1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, phases::phase_kernel<TN>, &cfg) != cudaSuccess || n < 1)
+        if (cudaOccupancyMaxActiveClusters(&n, phases::phase_kernel<TN, IN>, &cfg) != cudaSuccess || n < 1)
             return -1;
         pairs = n;
     }
@@ -34,19 +34,19 @@ static int phase_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int*
     return 0;
 }
 
-template <int TN>
+template <int TN, bool IN>
 static int launch(const phases::Params& p, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     int pairs = 0;
-    if (phase_config<TN>(cfg, attr, &pairs) != 0)
+    if (phase_config<TN, IN>(cfg, attr, &pairs) != 0)
         return -1;
     pairs = p.total < pairs ? p.total : pairs;
     pairs = p.max_pairs < pairs ? p.max_pairs : pairs;
     cfg.stream = s;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs));
-    if (cudaLaunchKernelEx(&cfg, phases::phase_kernel<TN>, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, phases::phase_kernel<TN, IN>, p) != cudaSuccess)
         return -1;
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -56,12 +56,14 @@ int phase_pairs()
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     int resident = 0;
-    return phase_config<256>(cfg, attr, &resident) == 0 ? resident : -1;
+    return phase_config<256, false>(cfg, attr, &resident) == 0 ? resident : -1;
 }
 
 int launch_phases(const phases::Params& p, cudaStream_t s)
 {
-    return p.tile_cols == 128 ? launch<128>(p, s) : launch<256>(p, s);
+    if (p.operands)
+        return p.tile_cols == 128 ? launch<128, true>(p, s) : launch<256, true>(p, s);
+    return p.tile_cols == 128 ? launch<128, false>(p, s) : launch<256, false>(p, s);
 }
 
 }  // namespace tffn

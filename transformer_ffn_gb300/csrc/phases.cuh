@@ -19,7 +19,7 @@
 // smaller tickets, so the launch finishes with any number of resident CTAs.
 //
 // The main loop is the FFN engine's (engine.cuh): clusters of two CTAs, a ring
-// of five 32 KiB stages per CTA (the sixth stage's room serves the epilogue), an A and a B loader and one MMA thread; a
+// of five or six 32 KiB stages per CTA, an A and a B loader and one MMA thread; a
 // scheduler thread claims the tickets.  The epilogue has eight warps, two per tensor
 // memory lane quadrant and so two per scheduler, each taking half of the
 // tile's columns, 32 at a time, through two 2 KiB staging buffers: a tile's
@@ -50,24 +50,28 @@ constexpr int SCHEDULER_WARP = 3 + EPI_WARPS;
 constexpr int NUM_THREADS = 32 * (4 + EPI_WARPS);
 // Arrivals that free a task slot: both CTAs' loaders and epilogue warps, the MMA thread.
 constexpr uint32_t TASK_CONSUMERS = 2 * (2 + EPI_WARPS) + 1;
+constexpr int MAX_STAGES = 8;
 constexpr int OUT_BUF_BYTES = 32 * 32 * 2;                 // 32 rows x 32 columns
 constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;   // 32 KiB
 constexpr int IN_BYTES = EPI_WARPS * 2 * OUT_BUF_BYTES;    // as much for the epilogue's own operands
 
-template <int TN>
+// IN: the launch has epilogues with operands of their own (a gradient's G and U,
+// a polynomial's C), whose buffers take the room of a stage.
+template <int TN, bool IN>
 struct Geo {
     static constexpr int STAGE_BYTES = A_STAGE_BYTES + TN / 2 * BK * 2;
-    static constexpr int STAGES = TN == 256 ? 5 : 6;       // 160 or 144 KiB
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + IN_BYTES + AUX_BYTES + 1024;
+    static constexpr int STAGES = TN == 256 ? (IN ? 5 : 6) : (IN ? 6 : 8);
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + (IN ? IN_BYTES : 0) + AUX_BYTES + 1024;
     static constexpr int PART_VEC = BM * TN / 4;           // float4 of one K part of a tile
     static constexpr int PART_WARP_VEC = PART_VEC / TILE_PARTS;
 };
-static_assert(Geo<256>::SMEM_BYTES <= 232448 && Geo<128>::SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(Geo<256, true>::SMEM_BYTES <= 232448 && Geo<256, false>::SMEM_BYTES <= 232448 &&
+                  Geo<128, true>::SMEM_BYTES <= 232448 && Geo<128, false>::SMEM_BYTES <= 232448,
+              "shared memory per CTA");
 
-template <int TN>
 struct Aux {
-    uint64_t full[Geo<TN>::STAGES];
-    uint64_t empty[Geo<TN>::STAGES];
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];
     uint64_t task_full[TASK_SLOTS];
@@ -78,7 +82,7 @@ struct Aux {
     uint32_t tmem_base;
     uint32_t abort;
 };
-static_assert(sizeof(Aux<128>) <= AUX_BYTES, "aux block fits");
+static_assert(sizeof(Aux) <= AUX_BYTES, "aux block fits");
 
 // A task: x = phase (-1: no more work), y = row tile, z = column tile,
 // w = batch * 256 + K part.
@@ -233,7 +237,7 @@ __device__ __forceinline__ bool next_task(AuxT& aux, const WaitCtx& w, Ring& r, 
 // pair holds two tickets beyond the one it loads, all larger, so the smallest
 // unfinished ticket is always some pair's current task.
 template <int TN>
-__device__ void run_scheduler(const Params& p, Aux<TN>& aux, const WaitCtx& w)
+__device__ void run_scheduler(const Params& p, Aux& aux, const WaitCtx& w)
 {
     Ring ring;
     uint32_t ticket = atomicAdd(&p.ctrl->ticket, 1u);
@@ -251,10 +255,10 @@ __device__ void run_scheduler(const Params& p, Aux<TN>& aux, const WaitCtx& w)
 }
 
 // A loader of one CTA.
-template <int TN>
-__device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+template <int TN, bool IN>
+__device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
 {
-    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
+    constexpr int STAGES = Geo<TN, IN>::STAGES, STAGE_BYTES = Geo<TN, IN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0;
     int32_t known = -1;
     Ring ring;
@@ -308,10 +312,10 @@ __device__ void run_a_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, con
                 wait_own(w, ptx::smem_u32(&aux.full[s]), static_cast<uint32_t>(last_phase[s]));
 }
 
-template <int TN>
-__device__ void run_b_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
+template <int TN, bool IN>
+__device__ void run_b_loader(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t rank)
 {
-    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
+    constexpr int STAGES = Geo<TN, IN>::STAGES, STAGE_BYTES = Geo<TN, IN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0;
     int32_t known = -1;
     Ring ring;
@@ -349,10 +353,10 @@ __device__ void run_b_loader(const Params& p, Aux<TN>& aux, uint8_t* stages, con
 }
 
 // ------------------------------------------------------------- leader: MMA
-template <int TN>
-__device__ void run_mma(const Params& p, Aux<TN>& aux, uint8_t* stages, const WaitCtx& w, uint32_t tmem_base)
+template <int TN, bool IN>
+__device__ void run_mma(const Params& p, Aux& aux, uint8_t* stages, const WaitCtx& w, uint32_t tmem_base)
 {
-    constexpr int STAGES = Geo<TN>::STAGES, STAGE_BYTES = Geo<TN>::STAGE_BYTES;
+    constexpr int STAGES = Geo<TN, IN>::STAGES, STAGE_BYTES = Geo<TN, IN>::STAGE_BYTES;
     uint32_t stage = 0, phase = 0, iter = 0;
     Ring ring;
     for (;;) {
@@ -753,11 +757,11 @@ __device__ __forceinline__ uint32_t epi_glu_grad(const Params& p, const Phase& f
     return sb;
 }
 
-template <int TN>
+template <int TN, bool IN>
 __device__ __forceinline__ uint32_t epilogue_tile(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
                                                bool mirror, uint32_t sb)
 {
-    if (f.epi == EPI_GLU_SAVE) {
+    if (!IN && f.epi == EPI_GLU_SAVE) {
         switch (f.act) {
         case TFFN_ACT_SILU: return epi_glu_save<TN, TFFN_ACT_SILU>(p, f, src, t, sb);
         case TFFN_ACT_GELU_TANH: return epi_glu_save<TN, TFFN_ACT_GELU_TANH>(p, f, src, t, sb);
@@ -765,22 +769,26 @@ __device__ __forceinline__ uint32_t epilogue_tile(const Params& p, const Phase& 
         default: return epi_glu_save<TN, TFFN_ACT_NONE>(p, f, src, t, sb);
         }
     }
-    if (f.epi == EPI_GLU_GRAD) {
-        switch (f.act) {
-        case TFFN_ACT_SILU: return epi_glu_grad<TFFN_ACT_SILU>(p, f, src, t, sb);
-        case TFFN_ACT_GELU_TANH: return epi_glu_grad<TFFN_ACT_GELU_TANH>(p, f, src, t, sb);
-        case TFFN_ACT_RELU: return epi_glu_grad<TFFN_ACT_RELU>(p, f, src, t, sb);
-        default: return epi_glu_grad<TFFN_ACT_NONE>(p, f, src, t, sb);
+    if constexpr (IN) {
+        if (f.epi == EPI_GLU_GRAD) {
+            switch (f.act) {
+            case TFFN_ACT_SILU: return epi_glu_grad<TFFN_ACT_SILU>(p, f, src, t, sb);
+            case TFFN_ACT_GELU_TANH: return epi_glu_grad<TFFN_ACT_GELU_TANH>(p, f, src, t, sb);
+            case TFFN_ACT_RELU: return epi_glu_grad<TFFN_ACT_RELU>(p, f, src, t, sb);
+            default: return epi_glu_grad<TFFN_ACT_NONE>(p, f, src, t, sb);
+            }
         }
+        if (f.aux0 != nullptr)
+            return epi_poly<true>(p, f, src, t, mirror, sb);
     }
-    return f.aux0 != nullptr ? epi_poly<true>(p, f, src, t, mirror, sb) : epi_poly<false>(p, f, src, t, mirror, sb);
+    return epi_poly<false>(p, f, src, t, mirror, sb);
 }
 
-template <int TN>
-__device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank,
+template <int TN, bool IN>
+__device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32_t tmem_base, uint32_t rank,
                              int warp, int lane, uint32_t out_stage, uint32_t in_stage)
 {
-    using G = Geo<TN>;
+    using G = Geo<TN, IN>;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);         // TMEM lanes [32 quad, 32 quad + 32)
     const int32_t group = (warp - 2) / 4;                          // half of the tile's columns
     const uint32_t part_warp = rank * EPI_WARPS + group * 4 + quad;
@@ -809,7 +817,7 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
         src.nparts = 0;
         src.part_vec = G::PART_VEC;
         const bool inside = t.row0 < f.rows && t.nchunks > 0;   // else this warp stores nothing
-        if (f.epi == EPI_GLU_GRAD && inside)
+        if (IN && f.epi == EPI_GLU_GRAD && inside)
             fetch_gu(f, t, 0);
         if (!wait_mbar(w, ptx::smem_u32(&aux.tmem_full[acc]), (iter >> 1) & 1u, SITE_TMEM_FULL))
             break;
@@ -855,7 +863,7 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
         }
         const bool mirror = f.sym != 0 && task.y != task.z * TN / BM;
         if (finish)
-            sb = epilogue_tile<TN>(p, f, src, t, mirror, sb);
+            sb = epilogue_tile<TN, IN>(p, f, src, t, mirror, sb);
         if (f.splits <= 1) {
             ptx::tc_fence_before();
             __syncwarp();
@@ -889,14 +897,14 @@ __device__ void run_epilogue(const Params& p, Aux<TN>& aux, const WaitCtx& w, ui
 }
 
 // ------------------------------------------------------------------- kernel
-template <int TN>
+template <int TN, bool IN>
 __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int STAGES = Geo<TN>::STAGES, RING_BYTES = STAGES * Geo<TN>::STAGE_BYTES;
-    Aux<TN>& aux = *reinterpret_cast<Aux<TN>*>(stages + RING_BYTES + OUT_BYTES + IN_BYTES);
+    constexpr int STAGES = Geo<TN, IN>::STAGES, RING_BYTES = STAGES * Geo<TN, IN>::STAGE_BYTES;
+    Aux& aux = *reinterpret_cast<Aux*>(stages + RING_BYTES + OUT_BYTES + (IN ? IN_BYTES : 0));
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -932,18 +940,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) phase_kernel(const __grid_cons
 
     if (warp == 0) {
         if (lane == 0)
-            run_a_loader<TN>(p, aux, stages, w, rank);
+            run_a_loader<TN, IN>(p, aux, stages, w, rank);
     } else if (warp == B_LOADER_WARP) {
         if (lane == 0)
-            run_b_loader<TN>(p, aux, stages, w, rank);
+            run_b_loader<TN, IN>(p, aux, stages, w, rank);
     } else if (warp == 1) {
         if (lane == 0 && rank == 0)
-            run_mma<TN>(p, aux, stages, w, tmem_base);
+            run_mma<TN, IN>(p, aux, stages, w, tmem_base);
     } else if (warp == SCHEDULER_WARP) {
         if (lane == 0 && rank == 0)
             run_scheduler<TN>(p, aux, w);
     } else {
-        run_epilogue<TN>(p, aux, w, tmem_base, rank, warp, lane,
+        run_epilogue<TN, IN>(p, aux, w, tmem_base, rank, warp, lane,
                      ptx::smem_u32(stages + RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES),
                      ptx::smem_u32(stages + RING_BYTES + OUT_BYTES) +
                          static_cast<uint32_t>((warp - 2) * 2 * OUT_BUF_BYTES));

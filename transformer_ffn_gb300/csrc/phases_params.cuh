@@ -73,6 +73,7 @@ struct Params {
     int32_t total;              // tickets
     int32_t tile_cols;          // columns of a tile: 256 or 128
     int32_t max_pairs;          // CTA pairs worth launching
+    int32_t operands;           // 1: phases with GLU_GRAD or with a C (and none with GLU_SAVE)
     DevCtrl* ctrl;
     uint32_t* counters;         // zero when a launch starts, zeroed again by the last CTA out
     int32_t n_counters;

@@ -294,9 +294,14 @@ int glu_train_forward(const void* X, const void* W1, const void* W3, const void*
     const Mat h = dense(ws.data + gs.h, M, O);
 
     // the tile width that is expected to be faster: a gated tile makes half its columns of H
+    // with a single band the gated product may be split too (two split phases
+    // share the partial tiles, so the second must wait for all of the first)
+    auto up_parts = [&](int64_t tn) {
+        return bands == 1 ? split_parts(div_up(O, tn / 2), div_up(N, BK), pairs, tn) : 1;
+    };
     auto cost = [&](int64_t tn) {
         const int64_t tiles = bands * div_up(P, tn), nk = div_up(O, BK);
-        return phase_us(bands * div_up(O, tn / 2), div_up(N, BK), 1, pairs, tn) +
+        return phase_us(bands * div_up(O, tn / 2), div_up(N, BK), up_parts(tn), pairs, tn) +
                phase_us(tiles, nk, split_parts(tiles, nk, pairs, tn), pairs, tn);
     };
     const int64_t tn = cost(128) < cost(256) ? 128 : 256;
@@ -324,7 +329,8 @@ int glu_train_forward(const void* X, const void* W1, const void* W3, const void*
     if (mp.failed)
         return TFFN_ERR_INVALID_ARG;
     const int parts = split_parts(phase_tiles(down, tn), down.nk[0], pairs, tn);
-    p.max_pairs = cap_pairs(std::max(phase_tiles(up, tn), phase_tiles(down, tn) * parts));
+    t.split(up, static_cast<int>(up_parts(tn)), reinterpret_cast<float*>(ws.data + gs.part));
+    p.max_pairs = cap_pairs(std::max(phase_tiles(up, tn) * up.splits, phase_tiles(down, tn) * parts));
     t.split(down, parts, reinterpret_cast<float*>(ws.data + gs.part));
     add_interleaved(t, up, down, bands, parts > 1 ? bands : band_group(bands, up.group_m, MAX_GROUPS));
     api_timing_start(s);
@@ -373,6 +379,7 @@ int glu_backward(const void* dY, const void* X, const void* W1, const void* W3, 
     };
     const int64_t tn = cost(128) < cost(256) ? 128 : 256;
     p.tile_cols = static_cast<int32_t>(tn);
+    p.operands = 1;
     // dH = dY W2^T, and from it dG, dU and H
     Phase up = make_phase(M, O, tn, P, 0, P);
     up.epi = phases::EPI_GLU_GRAD;
@@ -532,6 +539,7 @@ int muon_launch(const ApiSpace& ws, const MuonSpace& q, int64_t m, int64_t n, in
     const int64_t tn = step_us(128) < step_us(256) ? 128 : 256;
     const bool pair = q.mats == 6 && steps == STEPS_PER_LAUNCH && 3 * small_us(tn) < gram_us(tn) + update_us(tn);
     p.tile_cols = static_cast<int32_t>(tn);
+    p.operands = 1;
     // X as A and as B operand: K-major in one product, MN-major in the other
     int xa[2], xb[2], xc[2], xo[2];   // gram's A and B operands, the update's X operand, output
     for (int i = 0; i < 2; ++i) {
