@@ -76,7 +76,7 @@ struct Aux {
     uint64_t tmem_empty[2];
     uint64_t task_full[TASK_SLOTS];
     uint64_t task_empty[TASK_SLOTS];
-    uint64_t taken;                 // leader: the A loader has read the last task
+    uint64_t taken;                 // leader: the A loader copies the last task's operands
     uint64_t drain;
     int4 task[TASK_SLOTS];
     uint32_t tmem_base;
@@ -232,23 +232,24 @@ __device__ __forceinline__ bool next_task(AuxT& aux, const WaitCtx& w, Ring& r, 
 
 // ----------------------------------------------------------------- loaders
 // Scheduler (leader): claims tickets and hands each task to both CTAs' rings,
-// the next one as soon as the A loader has taken the last, so that a short
-// task's copies wait neither for a claim's round trip nor for its decoding.  A
-// pair holds two tickets beyond the one it loads, all larger, so the smallest
-// unfinished ticket is always some pair's current task.
+// the next one when the A loader begins to copy the last, so that a short task's
+// copies wait neither for a claim's round trip nor for its decoding.  Not
+// before: a pair that waits for its task's operands with another task in hand
+// may leave other pairs without one (of 64 tasks of 37 us on 76 pairs, thirty
+// had two: 146 us instead of 119).  A pair's ticket ahead is larger than its
+// current one, so the smallest unfinished ticket is always some pair's current
+// task.
 template <int TN>
 __device__ void run_scheduler(const Params& p, Aux& aux, const WaitCtx& w)
 {
     Ring ring;
-    uint32_t ticket = atomicAdd(&p.ctrl->ticket, 1u);
     for (uint32_t n = 0;; ++n) {
-        const int4 task = decode_ticket<TN>(p, static_cast<int32_t>(ticket));
+        const int4 task = decode_ticket<TN>(p, static_cast<int32_t>(atomicAdd(&p.ctrl->ticket, 1u)));
         if (!wait_mbar_cl(w, ptx::smem_u32(&aux.task_empty[ring.slot]), ring.phase ^ 1u, SITE_TASK_EMPTY))
             return;
         engine::publish_task(aux, ring, task);
         if (task.x < 0)
             return;
-        ticket = atomicAdd(&p.ctrl->ticket, 1u);
         if (!wait_mbar(w, ptx::smem_u32(&aux.taken), n & 1u, SITE_TASK_EMPTY))
             return;
     }
@@ -269,8 +270,6 @@ __device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const W
         int4 task;
         if (!next_task(aux, w, ring, rank, false, 0, task) || task.x < 0)
             break;
-        if (rank == 0)
-            ptx::mbar_arrive(ptx::smem_u32(&aux.taken));
         const Phase& f = p.ph[task.x];
         const int32_t batch = task_batch(task);
         const int32_t row0 = task.y * BM + static_cast<int32_t>(rank) * BM_CTA;
@@ -282,6 +281,8 @@ __device__ void run_a_loader(const Params& p, Aux& aux, uint8_t* stages, const W
         part_range(f, task_part(task), k0, k1);
         if (!wait_dep(p, w, f.dep_a, batch, task.y, known))
             break;
+        if (rank == 0)
+            ptx::mbar_arrive(ptx::smem_u32(&aux.taken));
         bool ok = true;
         for (int kb = k0; kb < k1; ++kb) {
             ok = wait_mbar(w, ptx::smem_u32(&aux.empty[stage]), phase ^ 1u, SITE_SMEM_EMPTY);
