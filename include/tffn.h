@@ -349,7 +349,10 @@ const char* tffn_status_string(int status);
  *                         publishes the flags of this 128-column H slice; the
  *                         waiting GEMM2 work then times out and the call
  *                         reports TFFN_ERR_TIMEOUT through tffn_check() (or
- *                         tffn_check_noalloc())
+ *                         tffn_check_noalloc()).  The training products
+ *                         (ffn_glu_forward_train, ffn_glu_backward,
+ *                         muon_orthogonalize past its small sides) never count
+ *                         this tile of their first product, with the same end
  *   TFFN_OPT_GROUP_M      row bands per raster group of the engine; 0
  *                         (default): 8 when N >= 8192, else 4 (the measured
  *                         optima on GB300)

@@ -171,3 +171,32 @@ def test_interleaved_with_inference(cuda_lib):
         cuda_lib.muon_orthogonalize(W1)
         assert torch.equal(cuda_lib.ffn_glu_forward_train(X, W1, W3, W2)[0], Y)
     cuda_lib.check()
+
+
+def test_wait_timeout_is_reported_and_recovered(cuda_lib):
+    """A tile that is never counted: the products that wait for it give up after
+    the limit, the call is reported, and the next calls are right again."""
+    ops = _operands()
+    X, W1, W3, W2, dY, m, _, _ = ops
+    Y, G, U = cuda_lib.ffn_glu_forward_train(X, W1, W3, W2)
+    calls = (lambda: cuda_lib.ffn_glu_forward_train(X, W1, W3, W2),
+             lambda: cuda_lib.ffn_glu_backward(dY, X, W1, W3, W2, G, U),
+             lambda: [cuda_lib.muon_orthogonalize(m)])
+    want = [call() for call in calls]
+    cuda_lib.check()
+    limit = cuda_lib.set_option(cuda_lib.OPT_WAIT_LIMIT_MS, 100)
+    try:
+        for call in calls:
+            cuda_lib.set_option(cuda_lib.OPT_SKIP_FLAG, 0)
+            call()
+            cuda_lib.set_option(cuda_lib.OPT_SKIP_FLAG, -1)
+            with pytest.raises(cuda_lib.TffnError) as e:
+                cuda_lib.check()
+            assert e.value.code == -4
+            cuda_lib.check()
+    finally:
+        cuda_lib.set_option(cuda_lib.OPT_SKIP_FLAG, -1)
+        cuda_lib.set_option(cuda_lib.OPT_WAIT_LIMIT_MS, limit)
+    for call, w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(call(), w))
+    cuda_lib.check()

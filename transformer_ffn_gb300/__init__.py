@@ -374,12 +374,14 @@ def layer_norm_forward(X, gamma, beta, residual=None, eps=1e-5, stream=None):
     if residual is not None:
         _check_tensor("residual", residual, dtype, shape, dev)
     s = _stream_of(stream, dev, (X, residual, gamma, beta))
-    Y, stats, *rest = _alloc(stream, dev, (shape, dtype), ((2, T), _F32), *(() if residual is None else ((shape, dtype),)))
-    mean, rstd = stats.unbind(0)
-    at = stats.data_ptr()
-    S = rest[0] if rest else X
+    if residual is None:
+        Y, mean, rstd = _alloc(stream, dev, (shape, dtype), ((T,), _F32), ((T,), _F32))
+        S, s_ptr = X, None
+    else:
+        Y, mean, rstd, S = _alloc(stream, dev, (shape, dtype), ((T,), _F32), ((T,), _F32), (shape, dtype))
+        s_ptr = S.data_ptr()
     rc = L.layer_norm_forward(X.data_ptr(), _addr(residual), _addr(gamma), _addr(beta), eps, _DTYPES[dtype],
-                              _DTYPES[par], T, N, Y.data_ptr(), S.data_ptr() if rest else None, at, at + 4 * T, s)
+                              _DTYPES[par], T, N, Y.data_ptr(), s_ptr, mean.data_ptr(), rstd.data_ptr(), s)
     if rc:
         _raise(rc, "layer_norm_forward")
     return Y, S, mean, rstd

@@ -258,6 +258,7 @@ int workspace(DeviceState& d, size_t need, cudaStream_t s, uint8_t** base)
             }
             const size_t bytes = align_up(need, size_t(64) << 20);
             if (cudaMalloc(&d.owned, bytes) != cudaSuccess) {
+                (void)cudaGetLastError();   // not to be taken for a later launch's
                 d.owned = nullptr;
                 return TFFN_ERR_CUDA;
             }

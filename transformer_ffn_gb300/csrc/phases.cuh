@@ -874,7 +874,8 @@ __device__ void run_epilogue(const Params& p, Aux& aux, const WaitCtx& w, uint32
         ++iter;
         // Count this warp's part of the tile once its stores are complete.  A
         // warp outside the matrix counts at once (with split K: in part 0).
-        if (f.done_base >= 0 && (finish || (!inside && task_part(task) == 0))) {
+        const bool skipped = task.x == 0 && task.y * f.n_tiles + task.z == p.skip_tile;
+        if (f.done_base >= 0 && !skipped && (finish || (!inside && task_part(task) == 0))) {
             if (lane == 0) {
                 ptx::bulk_wait_group<0>();
                 ptx::fence_proxy_async_global();

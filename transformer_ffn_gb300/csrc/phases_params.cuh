@@ -15,8 +15,9 @@ constexpr int EPI_WARPS = 8;                           // per CTA
 constexpr int MAX_MAPS = 36;
 constexpr int MAX_PHASES = 24;
 constexpr int TILE_PARTS = 2 * EPI_WARPS;              // epilogue warps that finish one tile
+
 enum Epilogue : int32_t {
-    EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16, read where it lies)
+    EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16)
     EPI_GLU_SAVE = 1,   // half the columns G, half U: out = {G, U, act(G) U}
     EPI_GLU_GRAD = 2,   // D = dH: out = {dG, dU, H} from the saved G, U
 };
@@ -45,7 +46,7 @@ struct Phase {
     int32_t nk[2];              // 64-deep k-blocks of the two K segments
     int8_t map_a[2], map_b[2];  // maps of the segments (GLU_SAVE: map_b = {W1, W3}, one segment)
     int8_t a_mn, b_mn;          // 1: MN-major operand
-    int8_t a4, b4;              // MN-major operand through one 4-D copy (else two 3-D boxes)
+    int8_t a4, b4;              // MN-major operand through one 4-D copy (else a 3-D box per 64 columns)
     int8_t f16;                 // operand type: 1 fp16, 0 bf16
     int8_t out_f16;             // output type
     int8_t out[3];              // output maps
@@ -79,6 +80,8 @@ struct Params {
     int32_t n_counters;
     int32_t pad_;
     uint64_t wait_limit_ns;
+    int32_t skip_tile;          // test fault injection: this tile of the first phase is never counted; -1: off
+    int32_t pad2_;
 };
 
 }  // namespace phases

@@ -211,6 +211,7 @@ int launch_table(PhaseParams& p, Table& t, const ApiSpace& ws, cudaStream_t s)
     p.ctrl = ws.ctrl;
     p.counters = ws.counters;
     p.wait_limit_ns = option_wait_limit_ns();
+    p.skip_tile = option_skip_flag();
     return launch_phases(p, s) == 0 ? TFFN_OK : TFFN_ERR_CUDA;
 }
 
