@@ -413,11 +413,13 @@ int pack(const void* G, int64_t batch, int64_t m, int64_t n, const double* part,
 
 }  // namespace muon
 
-int muon_norm_blocks(int64_t elems, int sms)
+int muon_norm_blocks(int64_t batch, int64_t elems, int sms)
 {
-    // eight values a thread at least, at most four blocks an SM
+    // of each entry: eight values a thread at least, at most four blocks an SM
+    // for all entries together (with four for each, eight entries of 4096 x 1024
+    // fp32 took 60 us instead of 24)
     return static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * 4, elems / (muon::THREADS * 8))));
+        std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * 4 / batch, elems / (muon::THREADS * 8))));
 }
 
 int muon_small_side() { return 64; }

@@ -482,7 +482,7 @@ MuonSpace muon_space(int64_t batch, int64_t m, int64_t n, int sms)
         o += static_cast<size_t>(pad_to(bytes, 256));
         return at;
     };
-    q.norm = take(batch * muon_norm_blocks(m * n, sms) * 8);
+    q.norm = take(batch * muon_norm_blocks(batch, m * n, sms) * 8);
     if (q.side <= muon_small_side()) {
         q.part = take(static_cast<int64_t>(muon_small_bytes(batch, q.side, std::max(m, n), sms)));
         q.total = o;
@@ -695,7 +695,7 @@ int muon_run(const void* G, int dtype, int64_t batch, int64_t m, int64_t n, int 
         return TFFN_ERR_CUDA;
     const bool f32 = dtype == TFFN_F32;
     double* part = reinterpret_cast<double*>(ws.data + q.norm);
-    const int blocks = muon_norm_blocks(m * n, sms);
+    const int blocks = muon_norm_blocks(batch, m * n, sms);
     if (launch_muon_norm(G, f32, batch, m * n, part, blocks, s) != 0)
         return TFFN_ERR_CUDA;
     if (q.side <= muon_small_side()) {

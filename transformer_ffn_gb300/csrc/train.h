@@ -46,7 +46,7 @@ int muon_small_side();
 size_t muon_small_bytes(int64_t batch, int64_t side, int64_t len, int sms);
 int launch_muon_small(const void* G, bool f32, int64_t batch, int64_t m, int64_t n, const double* norm, int blocks,
                       float eps, float* part, int steps, const float* abc, void* out, int sms, cudaStream_t s);
-int muon_norm_blocks(int64_t elems, int sms);
+int muon_norm_blocks(int64_t batch, int64_t elems, int sms);
 int launch_muon_norm(const void* G, bool f32, int64_t batch, int64_t elems, double* part, int blocks, cudaStream_t s);
 int launch_muon_pack(const void* G, bool f32, int64_t batch, int64_t m, int64_t n, const double* part, int blocks,
                      float scale, float eps, void* X, int64_t ld, int sms, cudaStream_t s);
