@@ -615,7 +615,7 @@ __device__ __forceinline__ void read_row(uint32_t buf, int lane, uint4 (&v)[4])
                      : "memory");
 }
 
-// out = alpha D + beta C + diag I (AUX: with the last two).
+// out = alpha D + beta C + diag I (AUX: with the last two; C may be absent).
 template <bool AUX>
 __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, const Source& src, const TileCtx& t,
                                              bool mirror, uint32_t sb)
@@ -626,11 +626,12 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
     const CUtensorMap* map_t = &p.map[f.out_t];
     // C's rows are 16-byte aligned and padded to 8 columns; read one chunk ahead
     const __half* c_base = static_cast<const __half*>(f.aux0) + t.batch * f.aux_batch;
+    const bool has_c = f.aux0 != nullptr;
     auto load_c = [&](int c) {
         fetch_chunk(t.in, c_base, f.aux_ld, f.rows, f.ncols, t, t.col0 + c * 32);
         fetch_commit();
     };
-    if (AUX)
+    if (AUX && has_c)
         load_c(0);
 #pragma unroll 1
     for (int c = 0; c < t.nchunks; ++c) {
@@ -639,20 +640,25 @@ __device__ __forceinline__ uint32_t epi_poly(const Params& p, const Phase& f, co
         float v[32];
         source32(src, t.tcol + c * 32, c, v);
         if (AUX) {
-            uint4 cv[4];
-            fetch_wait();
-            read_row(t.in, t.lane, cv);
-            __syncwarp();
-            if (c + 1 < t.nchunks)
-                load_c(c + 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t cw[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
+            for (int i = 0; i < 32; ++i)
+                v[i] *= alpha;
+            if (has_c) {
+                uint4 cv[4];
+                fetch_wait();
+                read_row(t.in, t.lane, cv);
+                __syncwarp();
+                if (c + 1 < t.nchunks)
+                    load_c(c + 1);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&cw[q]));
-                    v[j * 8 + q * 2] = fmaf(alpha, v[j * 8 + q * 2], beta * cf.x);
-                    v[j * 8 + q * 2 + 1] = fmaf(alpha, v[j * 8 + q * 2 + 1], beta * cf.y);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t cw[4] = {cv[j].x, cv[j].y, cv[j].z, cv[j].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&cw[q]));
+                        v[j * 8 + q * 2] = fmaf(beta, cf.x, v[j * 8 + q * 2]);
+                        v[j * 8 + q * 2 + 1] = fmaf(beta, cf.y, v[j * 8 + q * 2 + 1]);
+                    }
                 }
             }
             if (x == t.row0) {   // this box is on the diagonal: column = lane
@@ -779,7 +785,7 @@ __device__ __forceinline__ uint32_t epilogue_tile(const Params& p, const Phase& 
             default: return epi_glu_grad<TFFN_ACT_NONE>(p, f, src, t, sb);
             }
         }
-        if (f.aux0 != nullptr)
+        if (f.aux0 != nullptr || f.diag != 0.0f)
             return epi_poly<true>(p, f, src, t, mirror, sb);
     }
     return epi_poly<false>(p, f, src, t, mirror, sb);

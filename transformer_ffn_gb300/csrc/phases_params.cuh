@@ -17,7 +17,7 @@ constexpr int MAX_PHASES = 24;
 constexpr int TILE_PARTS = 2 * EPI_WARPS;              // epilogue warps that finish one tile
 
 enum Epilogue : int32_t {
-    EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16)
+    EPI_POLY = 0,       // out = alpha D + beta C + diag I (C fp16, nullable)
     EPI_GLU_SAVE = 1,   // half the columns G, half U: out = {G, U, act(G) U}
     EPI_GLU_GRAD = 2,   // D = dH: out = {dG, dU, H} from the saved G, U
 };
