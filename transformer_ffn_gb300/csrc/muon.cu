@@ -171,10 +171,11 @@ __global__ void __launch_bounds__(THREADS) muon_pack_kernel(const T* G, int64_t 
 // parts of the long side, and Q with its product.  Every block of the second
 // runs the whole iteration (18 products of side^3, each about 3 us at 64 and
 // bound by shared-memory loads and their latency) before its share of the
-// product, which costs nothing beside handing Q over.  Measured: 16 x 300 22 us,
-// 64 x 4096 72 us, where fifteen dependent phases of tensor-core products take
-// 75 us and more; and fp32 keeps what fp16 loses where few entries make a
-// matrix (3e-3 of its norm with 16 rows).
+// product, which costs nothing beside handing Q over.  Measured against the
+// tensor-core products' fifteen dependent phases: 16 x 300 22 us (63), 32 x 2000
+// 25 (80), 64 x 64 55 (60), 64 x 4096 72 (95), three of 5288 x 48 86 (111); the
+// time grows with the side's cube, so 64 is where it ends.  And fp32 keeps what
+// fp16 loses where few entries make a matrix (3e-3 of its norm with 16 rows).
 constexpr int CHUNK = 64;   // long-side elements in shared memory at a time
 
 // One chunk of an entry, [S short][CHUNK long], scaled; zero outside.

@@ -177,7 +177,11 @@ constexpr int THREADS_PER_SM = 512;   // 128 registers a thread, all of shared m
 // barrier; the only ones are the row sums', once a turn, and a turn reads its
 // rows again from shared memory instead of holding them in registers.  A block
 // with a row each and its loads in registers reached 4.5-4.8 TB/s on 8192
-// columns, this form 6.3.
+// columns, this form 5.8 forward and 6.3 backward (16384 x 8192 bf16 with the
+// residual, 181 and 169 us; HBM takes writes, half of the forward's traffic, at
+// 3.9).  A warp's rows take one row a turn (it has no barrier to share), blocks
+// two; 32768 x 4096 165 us backward, 131072 x 512 98 us, odd 4093 columns in
+// 4-byte words 332 us.
 template <typename T, int VW, int TPR, int NV, int TENSORS>
 struct Shape {
     static constexpr int THREADS = TPR == 32 ? 256 : TPR;
